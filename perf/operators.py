@@ -304,7 +304,7 @@ def _plain_evict(s):
     late = (j >= kv - recent) & (j < kv)
     key = torch.where(late, torch.full((), float("inf"), device="cuda"), s["weights"])
     key = torch.where(j < kv, key, torch.full((), -1.0, device="cuda"))
-    order = key.sort(-1, descending=True, stable=True).indices[..., :budget]
+    order = torch.sort(key, dim=-1, descending=True, stable=True).indices[..., :budget]
     order = torch.where(torch.arange(order.shape[-1], device="cuda") < kv, order, torch.full_like(order, width))
     kept = order.sort(-1).values
     new = torch.minimum(s["kv_lens"], torch.full_like(s["kv_lens"], budget))
