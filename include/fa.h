@@ -227,6 +227,157 @@ FA_API fa_status fa_pad(const void *x, const int64_t *indices, int64_t nnz, int6
                  int64_t row_bytes, void *out, void *stream);
 
 /*
+ * RMS norm of queries and keys for each head, then the position rotation, in one pass:
+ *   n = w * x / sqrt(mean(x^2) + eps) over the D values of a head,
+ *   then each pair (a, b) of the first rot_dim values becomes (a c - b s, b c + a s) with the
+ *   cosine c and sine s of the token's position; the pairs are (i, i + rot_dim/2), or (2i, 2i + 1)
+ *   when `interleaved` is nonzero; values from rot_dim on are not turned. 32-bit arithmetic, one
+ *   rounding at the end. (The pages give attention from q and k on and have no counterpart to
+ *   this and the following operators around a cache.)
+ *   q, k         n token rows of Hq and Hkv heads of D values (element type `dtype`); the heads of a
+ *                token are contiguous, tokens lie q_stride / k_stride elements apart (views of a
+ *                fused projection work as they are).
+ *   q_weight,
+ *   k_weight     D weights each, of `dtype` or (weight_fp32 nonzero) float32; NULL: ones.
+ *   cos_sin      float32 (max_pos, rot_dim): rot_dim/2 cosines, then rot_dim/2 sines of each position.
+ *   positions    device int64 [n], each in [0, max_pos). One outside reads row 0 instead (that
+ *                output is wrong) and leaves FA_ERR_INDEX for fa_device_status.
+ *   q_out, k_out the results, token strides of their own; each may be its input itself (same pointer
+ *                and stride), and must not overlap it otherwise.
+ * rot_dim: a multiple of 16, 16 <= rot_dim <= D. Strides: multiples of 8 elements, at least H * D
+ * (FA_ERR_ALIGN). Every pointer but positions 16-byte aligned. eps >= 0. n == 0 is a successful no-op.
+ */
+FA_API fa_status fa_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                 const void *q_weight, const void *k_weight, int weight_fp32,
+                                 const float *cos_sin, int64_t max_pos, int rot_dim,
+                                 const int64_t *positions, void *q_out, int64_t q_out_stride, void *k_out,
+                                 int64_t k_out_stride, int64_t n, int Hq, int Hkv, int D, float eps,
+                                 int interleaved, fa_dtype dtype, void *stream);
+
+/*
+ * Gradients of fa_qk_norm_rope from the gradients of its outputs (the norm is formed again from q
+ * and k, so nothing has to be kept from the forward).
+ *   q, k, the weights, cos_sin, positions, eps, interleaved: as in the forward.
+ *   dq_out, dk_out   gradients of q_out and k_out (token strides of their own).
+ *   dq, dk           gradients of q and k, element type `dtype` (token strides of their own; dq may be
+ *                    dq_out itself and dk dk_out; no other overlap).
+ *   dq_weight,
+ *   dk_weight        float32 [D] gradients of the weights, summed over tokens and heads in a fixed
+ *                    order; either may be NULL.
+ *   workspace        fa_qk_norm_rope_bwd_workspace(D) bytes, 16-byte aligned (may be NULL when both
+ *                    weight gradients are). Calls that overlap on the GPU need one each.
+ * n == 0 writes zero weight gradients.
+ */
+FA_API int64_t fa_qk_norm_rope_bwd_workspace(int D);
+FA_API fa_status fa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                     const void *q_weight, const void *k_weight, int weight_fp32,
+                                     const float *cos_sin, int64_t max_pos, int rot_dim,
+                                     const int64_t *positions, const void *dq_out, int64_t dq_out_stride,
+                                     const void *dk_out, int64_t dk_out_stride, void *dq, int64_t dq_stride,
+                                     void *dk, int64_t dk_stride, float *dq_weight, float *dk_weight,
+                                     void *workspace, int64_t workspace_bytes, int64_t n, int Hq, int Hkv,
+                                     int D, float eps, int interleaved, fa_dtype dtype, void *stream);
+
+/*
+ * fa_qk_norm_rope where a cache is kept: q is normed and turned into q_out, k is normed and turned
+ * into its token's place in the key pages, v is copied into the value pages.
+ *   q, k, v      packed new tokens: sequence b's are rows [cu_seqlens[b], cu_seqlens[b + 1]).
+ *   cu_seqlens   device int32 [num_seqs + 1], non-decreasing. Rows of no sequence (at and after
+ *                cu_seqlens[num_seqs]) are left as they are.
+ *   kv_lens      device int32 [num_seqs]: each sequence's keys with the new ones; new token i of n
+ *                goes to slot kv_lens[b] - n + i. A slot outside the table or a table entry
+ *                outside the pool: that token's k and v are not written and FA_ERR_INDEX is left for
+ *                fa_device_status.
+ *   positions    device int64 [n] as above, or NULL: each token's slot is its position (they differ once
+ *                keys have been evicted).
+ *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
+ *                of (page_size, Hkv, D).
+ * The rest as fa_qk_norm_rope.
+ */
+FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                       const void *v, int64_t v_stride, const void *q_weight,
+                                       const void *k_weight, int weight_fp32, const float *cos_sin,
+                                       int64_t max_pos, int rot_dim, const int64_t *positions, void *q_out,
+                                       int64_t q_out_stride, void *k_cache, void *v_cache,
+                                       const int32_t *block_table, int max_blocks_per_seq, int page_size,
+                                       int num_pages, const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                       int num_seqs, int64_t n, int Hq, int Hkv, int D, float eps,
+                                       int interleaved, fa_dtype dtype, void *stream);
+
+/*
+ * Attention of each sequence's new tokens over its paged cache: prompts in chunks, single tokens,
+ * and batches of both.
+ *   q            (total, Hq, D) packed new tokens; sequence b owns rows [cu_seqlens[b],
+ *                cu_seqlens[b + 1]), n of them. Hq is a multiple of Hkv; query heads h * Hq/Hkv ...
+ *                share key head h.
+ *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
+ *                of (page_size, Hkv, D). Entries past ceil(kv_lens[b] / page_size) are never read;
+ *                what a page holds past the sequence's last key does not matter (NaN included).
+ *   kv_lens      device int32 [num_seqs]: keys of each sequence, the new tokens' own included.
+ *                Sequences may share pages.
+ *   causal       nonzero: new token i of n sees keys 0 .. kv_lens[b] - n + i (aligned at the end);
+ *                zero: all of them. A row that sees no key gets out = 0 and lse = -inf.
+ *   max_q_len    the most new tokens of a sequence. It chooses the kernel and the workspace's size, not the
+ *                result.
+ *   out          (total, Hq, D); lse (Hq, total) float32 or NULL. Rows of no sequence are left as
+ *                they are.
+ *   workspace    fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len) bytes, 256-byte aligned, contents
+ *                of no matter. Calls that overlap on the GPU (other streams, graphs replayed at the same
+ *                time) need one each.
+ * Offsets and lengths that do not fit total or the table are cut to it, and FA_ERR_INDEX is left for
+ * fa_device_status; the same for a table entry outside the pool, where page 0 is read instead.
+ * total * Hq / Hkv < 2^31. total == 0 or num_seqs == 0 is a successful no-op.
+ */
+FA_API int64_t fa_fwd_paged_chunk_workspace(int Hq, int Hkv, int D, int max_q_len);
+FA_API fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *block_table, int max_blocks_per_seq, int page_size,
+                                    int num_pages, const int32_t *cu_seqlens, const int32_t *kv_lens,
+                                    int num_seqs, int total, int max_q_len, void *out, float *lse,
+                                    void *workspace, int64_t workspace_bytes, int Hq, int Hkv, int D,
+                                    float scale, int causal, fa_dtype dtype, void *stream);
+
+/*
+ * Attention weight that each cached key received from a call's new tokens, added to a running sum:
+ *   weights[b, h, j] += sum over the rows (new token i, query head of key head h's group) that see
+ *   key j of exp(scale * q.k_j - lse).
+ *   q, k_cache, block_table, cu_seqlens, kv_lens, max_q_len, scale, causal: as fa_fwd_paged_chunk.
+ *   lse          (Hq, total) float32 that fa_fwd_paged_chunk returned for the same arguments (-inf
+ *                rows give nothing).
+ *   weights      float32 (num_seqs, Hkv, width), width >= max_blocks_per_seq * page_size; slots at and
+ *                past kv_lens[b] are not touched. Each sum is formed in a fixed order.
+ * Calls that overlap on the GPU must not share `weights`.
+ */
+FA_API fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t *block_table,
+                                      int max_blocks_per_seq, int page_size, int num_pages,
+                                      const int32_t *cu_seqlens, const int32_t *kv_lens, int num_seqs,
+                                      int total, int max_q_len, const float *lse, float *weights,
+                                      int64_t width, int Hq, int Hkv, int D, float scale, int causal,
+                                      fa_dtype dtype, void *stream);
+
+/*
+ * Eviction from a paged cache: every sequence and key head of more than `budget` keys keeps its last
+ * `recent` keys and, of the others, the budget - recent of most accumulated weight (equal weights:
+ * the lower slot; NaN counts as the largest). The kept keys' rows are closed up to slots 0 ..
+ * budget - 1 in their order, in place, K and V; each key head keeps keys of its own.
+ *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
+ *                of (page_size, Hkv, D). A sequence of more than `budget` keys must not share its
+ *                first ceil(kv_lens[b] / page_size) pages with another, nor name one twice.
+ *   kv_lens      device int32 [B] keys of each sequence.
+ *   weights      float32 (B, Hkv, width) accumulated weights, width >= max_blocks_per_seq * page_size.
+ *   kept         int32 (B, Hkv, budget) output: the old slot of each kept key, rising, then -1.
+ *   new_lens     int32 [B] output: min(kv_lens[b], budget).
+ *   new_weights  float32 (B, Hkv, width) output: the kept keys' weights in their new slots, zeros after.
+ * 1 <= budget <= width < 2^31, 0 <= recent <= budget. new_weights and new_lens are not weights and kv_lens
+ * themselves. Lengths that do not fit the table are cut to it and FA_ERR_INDEX is left for fa_device_status;
+ * a row whose table entry is outside the pool does not move (FA_ERR_INDEX too).
+ */
+FA_API fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_table,
+                                int max_blocks_per_seq, int page_size, int num_pages,
+                                const int32_t *kv_lens, const float *weights, int64_t width, int budget,
+                                int recent, int32_t *kept, int32_t *new_lens, float *new_weights, int B,
+                                int Hkv, int D, fa_dtype dtype, void *stream);
+
+/*
  * Device-side status of earlier launches: returns FA_OK or the first FA_ERR_TIMEOUT /
  * FA_ERR_INDEX that a kernel of this library recorded on the current device since the last
  * call, and clears it. `where` (may be NULL) receives a kernel-specific location code.

@@ -8,6 +8,11 @@ built, every call raises.
     out, lse = fa_varlen_fwd(q, k, v, cu_seqlens, max_seqlen)        # packed (total, H, D)
     out, lse = fa_fwd_paged(q, k_cache, v_cache, block_table)        # K/V in a page pool
     dq, dk, dv = fa_bwd(q, k, v, out, dout, lse, causal=True)        # gradients (recomputation)
+    q, k     = fa_qk_norm_rope(q, k, wq, wk, cos_sin, positions)     # norm of q and k, position rotation
+    q        = fa_qk_norm_rope_paged(q, k, v, ..., k_cache, v_cache, ...)  # the same into a paged cache
+    out, lse = fa_fwd_paged_chunk(q, k_cache, v_cache, ...)          # new tokens over a paged cache
+    weights  = fa_paged_key_weights(q, k_cache, ..., lse, weights)   # weight that each cached key received
+    kept, kv_lens, weights = fa_paged_evict(k_cache, v_cache, ...)   # keep the keys of most weight
     x_unpad  = fa_unpad(x, indices)                                  # (B, L, H, D) -> (nnz, H, D)
     x_pad    = fa_pad(x_unpad, indices, batch, total_len)            # (nnz, H, D) -> (B, L, H, D)
 """
@@ -58,6 +63,23 @@ def lib() -> ctypes.CDLL:
         L.fa_unpad_qkv.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp]
         L.fa_varlen_fwd_padded.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i64, vp, vp, i32, i32, f32, i32, i32,
                                            vp]
+        L.fa_qk_norm_rope.argtypes = [vp, i64, vp, i64, vp, vp, i32, vp, i64, i32, vp, vp, i64, vp, i64, i64, i32, i32, i32,
+                                      f32, i32, i32, vp]
+        L.fa_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp, i32, vp, i64, i32, vp, vp, i64, vp, i64, vp, i64, vp,
+                                          i64, vp, vp, vp, i64, i64, i32, i32, i32, f32, i32, i32, vp]
+        L.fa_qk_norm_rope_paged.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, i32, vp, i64, i32, vp, vp, i64, vp, vp, vp,
+                                            i32, i32, i32, vp, vp, i32, i64, i32, i32, i32, f32, i32, i32, vp]
+        L.fa_fwd_paged_chunk.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, i64, i32, i32,
+                                         i32, f32, i32, i32, vp]
+        L.fa_paged_key_weights.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, i64, i32, i32, i32,
+                                           f32, i32, i32, vp]
+        L.fa_paged_evict.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i64, i32, i32, vp, vp, vp, i32, i32, i32, i32, vp]
+        for f in (L.fa_qk_norm_rope, L.fa_qk_norm_rope_bwd, L.fa_qk_norm_rope_paged, L.fa_fwd_paged_chunk,
+                  L.fa_paged_key_weights, L.fa_paged_evict):
+            f.restype = ctypes.c_int
+        L.fa_qk_norm_rope_bwd_workspace.argtypes = [i32]
+        L.fa_fwd_paged_chunk_workspace.argtypes = [i32, i32, i32, i32]
+        L.fa_qk_norm_rope_bwd_workspace.restype = L.fa_fwd_paged_chunk_workspace.restype = i64
         L.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), vp]
         L.fa_selftest_bounded_wait.argtypes = [ctypes.c_uint64, vp]
         for f in (L.fa_fwd, L.fa_fwd_paged, L.fa_bwd, L.fa_bwd_noalloc, L.fa_varlen_bwd, L.fa_varlen_fwd, L.fa_varlen_fwd_padded, L.fa_unpad, L.fa_unpad_qkv, L.fa_pad,
@@ -401,6 +423,272 @@ def fa_pad(x: torch.Tensor, indices: torch.Tensor, batch: int, total_len: int,
                           _stream(stream))
     _check(st, "fa_pad")
     return out
+
+
+_no_context = contextlib.nullcontext()
+
+
+def _on_stream(t: torch.Tensor, stream):
+    """The operands' device and, where one is given, `stream` made current, so that what the call
+    allocates (results, workspace) belongs to the stream that uses it."""
+    if stream is None:
+        return _on_device(t) if t.get_device() != torch.cuda.current_device() else _no_context
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _heads(name: str, t: torch.Tensor, dim0: Optional[int] = None) -> Tuple[int, int]:
+    """(token rows, elements from one to the next) of a (..., H, D) tensor whose heads are contiguous
+    in a token and whose tokens lie at one stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() < 3:
+        raise ValueError(f"{name} must be (..., heads, head dim)")
+    H, D = t.shape[-2:]
+    st = t.stride()
+    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    n, stride = 1, H * D
+    for size, step in zip(reversed(t.shape[:-2]), reversed(st[:-2])):
+        if size == 1:
+            continue
+        if n == 1:
+            stride = step
+        elif step != stride * n:
+            raise ValueError(f"the tokens of {name} must lie at one stride")
+        n *= size
+    return (n if t.numel() else 0), stride
+
+
+def _norm_args(q, k, q_weight, k_weight, cos_sin, positions):
+    """Checks of what the norm entry points share -> (n, q stride, k stride, weights are float32)."""
+    n, qs = _heads("q", q)
+    nk, ks = _heads("k", k)
+    if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1] or k.dtype != q.dtype:
+        raise ValueError("q and k must share their leading shape, head dim and dtype")
+    w32 = False
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        _cuda_contig(name, w)
+        if tuple(w.shape) != (q.shape[-1],) or w.dtype not in (q.dtype, torch.float32):
+            raise ValueError(f"{name} must be ({q.shape[-1]},) of float32 or q's dtype")
+        w32 = w.dtype == torch.float32
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must share one dtype")
+    _cuda_contig("cos_sin", cos_sin)
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise ValueError("cos_sin must be float32 (positions, rot_dim)")
+    if positions is not None:
+        _cuda_contig("positions", positions)
+        if positions.dtype != torch.int64 or positions.shape != q.shape[:-2]:
+            raise ValueError("positions must be int64 of q's leading shape")
+    _same_device(q, k, q_weight, k_weight, cos_sin, positions)
+    return n, qs, ks, w32
+
+
+def fa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
+                    cos_sin: torch.Tensor, positions: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                    q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of q (..., Hq, D) and k (..., Hkv, D) for each head, weights (D,) or None, then the
+    rotation by cos_sin[positions] (float32 (positions, rot_dim): cosines, then sines). q and k may be
+    views of a fused projection. q_out and k_out may be q and k themselves."""
+    n, qs, ks, w32 = _norm_args(q, k, q_weight, k_weight, cos_sin, positions)
+    if positions is None:
+        raise ValueError("positions must be given")
+    dt = _dtype_code(q)
+    with _on_stream(q, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        for name, o, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+            _shape(name, o, like.shape, like.dtype)
+        qos, kos = _heads("q_out", q_out)[1], _heads("k_out", k_out)[1]
+        _same_device(q, q_out, k_out)
+        st = lib().fa_qk_norm_rope(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), w32, _ptr(cos_sin),
+                                   cos_sin.shape[0], cos_sin.shape[1], _ptr(positions), _ptr(q_out), qos, _ptr(k_out), kos,
+                                   n, q.shape[-2], k.shape[-2], q.shape[-1], float(eps), bool(interleaved), dt, _stream(None))
+    _check(st, "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def fa_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor],
+                        k_weight: Optional[torch.Tensor], cos_sin: torch.Tensor, positions: torch.Tensor,
+                        dq_out: torch.Tensor, dk_out: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                        stream=None):
+    """Gradients of fa_qk_norm_rope: (dq, dk, dq_weight, dk_weight), the weights' in float32 (None where
+    the weight is None)."""
+    n, qs, ks, w32 = _norm_args(q, k, q_weight, k_weight, cos_sin, positions)
+    if positions is None:
+        raise ValueError("positions must be given")
+    _shape("dq_out", dq_out, q.shape, q.dtype)
+    _shape("dk_out", dk_out, k.shape, k.dtype)
+    dqs, dks = _heads("dq_out", dq_out)[1], _heads("dk_out", dk_out)[1]
+    _same_device(q, dq_out, dk_out)
+    Hq, Hkv, D = q.shape[-2], k.shape[-2], q.shape[-1]
+    dt = _dtype_code(q)
+    with _on_stream(q, stream):
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        dwq = None if q_weight is None else torch.empty(D, dtype=torch.float32, device=q.device)
+        dwk = None if k_weight is None else torch.empty(D, dtype=torch.float32, device=q.device)
+        size = lib().fa_qk_norm_rope_bwd_workspace(D) if dwq is not None or dwk is not None else 0
+        ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+        st = lib().fa_qk_norm_rope_bwd(_ptr(q), qs, _ptr(k), ks, _ptr(q_weight), _ptr(k_weight), w32, _ptr(cos_sin),
+                                       cos_sin.shape[0], cos_sin.shape[1], _ptr(positions), _ptr(dq_out), dqs, _ptr(dk_out),
+                                       dks, _ptr(dq), Hq * D, _ptr(dk), Hkv * D, _ptr(dwq), _ptr(dwk), _ptr(ws), size, n, Hq,
+                                       Hkv, D, float(eps), bool(interleaved), dt, _stream(None))
+    _check(st, "fa_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def _paged_args(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens):
+    """Checks of a packed q over page pools -> (Hkv, sequences)."""
+    for n, t in (("k_cache", k_cache), ("block_table", block_table), ("kv_lens", kv_lens)):
+        _cuda_contig(n, t)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be (num_pages, page_size, Hkv, D)")
+    if v_cache is not None:
+        _cuda_contig("v_cache", v_cache)
+        if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+            raise ValueError("k_cache and v_cache must share one shape and dtype")
+    if kv_lens.dtype != torch.int32 or kv_lens.dim() != 1:
+        raise ValueError("kv_lens must be a 1-D int32 tensor")
+    num = kv_lens.shape[0]
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != num:
+        raise ValueError("block_table must be an int32 (sequences, max_blocks_per_seq) tensor")
+    if q is not None:
+        _cuda_contig("cu_seqlens", cu_seqlens)
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != num + 1:
+            raise ValueError("cu_seqlens must be int32 with one more entry than kv_lens")
+        if q.dim() != 3 or q.shape[-1] != k_cache.shape[3] or q.dtype != k_cache.dtype:
+            raise ValueError("q must be (total, Hq, D) with the caches' head dim and dtype")
+    _same_device(k_cache, q, v_cache, block_table, cu_seqlens, kv_lens)
+    return k_cache.shape[2], num
+
+
+def fa_qk_norm_rope_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
+                          k_weight: Optional[torch.Tensor], cos_sin: torch.Tensor, positions: Optional[torch.Tensor],
+                          k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                          cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                          q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fa_qk_norm_rope of packed new tokens q (total, Hq, D), k and v (total, Hkv, D), with k and v
+    written into the pages: new token i of sequence b's n goes to slot kv_lens[b] - n + i (kv_lens
+    counts the new tokens). positions None: the slot. Returns q_out."""
+    n, qs, ks, w32 = _norm_args(q, k, q_weight, k_weight, cos_sin, positions)
+    Hkv, num = _paged_args(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens)
+    if k.shape[1] != Hkv or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be (total, Hkv, D) like the caches' rows")
+    vs = _heads("v", v)[1]
+    _same_device(q, k_cache, v)
+    dt = _dtype_code(q)
+    with _on_stream(q, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _shape("q_out", q_out, q.shape, q.dtype)
+        qos = _heads("q_out", q_out)[1]
+        _same_device(q, q_out)
+        st = lib().fa_qk_norm_rope_paged(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight), _ptr(k_weight), w32,
+                                         _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], _ptr(positions), _ptr(q_out), qos,
+                                         _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
+                                         k_cache.shape[1], k_cache.shape[0], _ptr(cu_seqlens), _ptr(kv_lens), num, n,
+                                         q.shape[1], Hkv, q.shape[2], float(eps), bool(interleaved), dt, _stream(None))
+    _check(st, "fa_qk_norm_rope_paged")
+    return q_out
+
+
+def fa_fwd_paged_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                       cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int,
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       scale: Optional[float] = None, causal: bool = True, return_lse: bool = True,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of packed new tokens q (total, Hq, D) over their sequences' pages: k_cache, v_cache
+    (num_pages, page_size, Hkv, D), int32 block_table (B, max_blocks_per_seq), cu_seqlens (B + 1) and
+    kv_lens (B), which counts the new tokens -> out (total, Hq, D), lse (Hq, total) fp32. `workspace`
+    (uint8, of fa_fwd_paged_chunk_workspace(...) bytes) is allocated by the call unless given."""
+    Hkv, num = _paged_args(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens)
+    _cuda_contig("q", q)
+    total, Hq, D = q.shape
+    dt = _dtype_code(q)
+    size = lib().fa_fwd_paged_chunk_workspace(Hq, Hkv, D, int(max_q_len))
+    with _on_stream(q, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _like("out", out, q.shape, q.dtype)
+        if return_lse and lse is None:
+            lse = torch.empty((Hq, total), device=q.device, dtype=torch.float32)
+        elif lse is not None:
+            _like("lse", lse, (Hq, total), torch.float32)
+        if workspace is None:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        else:
+            _cuda_contig("workspace", workspace)
+        _same_device(q, out, lse, workspace)
+        st = lib().fa_fwd_paged_chunk(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
+                                      k_cache.shape[1], k_cache.shape[0], _ptr(cu_seqlens), _ptr(kv_lens), num, total,
+                                      int(max_q_len), _ptr(out), _ptr(lse), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), Hq, Hkv, D,
+                                      float(scale) if scale else 0.0, bool(causal), dt, _stream(None))
+    _check(st, "fa_fwd_paged_chunk")
+    return out, lse
+
+
+def fa_fwd_paged_chunk_workspace(Hq: int, Hkv: int, D: int, max_q_len: int) -> int:
+    """Bytes of fa_fwd_paged_chunk's workspace."""
+    return lib().fa_fwd_paged_chunk_workspace(int(Hq), int(Hkv), int(D), int(max_q_len))
+
+
+def fa_paged_key_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                         kv_lens: torch.Tensor, max_q_len: int, lse: torch.Tensor, weights: torch.Tensor,
+                         scale: Optional[float] = None, causal: bool = True, stream=None) -> torch.Tensor:
+    """Adds to weights (B, Hkv, width) float32 the attention weight that each cached key received from
+    the new tokens q, lse being what fa_fwd_paged_chunk returned for them. Returns weights."""
+    Hkv, num = _paged_args(q, k_cache, None, block_table, cu_seqlens, kv_lens)
+    _cuda_contig("q", q)
+    total, Hq, D = q.shape
+    _like("lse", lse, (Hq, total), torch.float32)
+    _cuda_contig("weights", weights)
+    if weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[0] != num or weights.shape[1] != Hkv:
+        raise ValueError("weights must be float32 (sequences, Hkv, width)")
+    _same_device(q, lse, weights)
+    dt = _dtype_code(q)
+    with _on_stream(q, stream):
+        st = lib().fa_paged_key_weights(_ptr(q), _ptr(k_cache), _ptr(block_table), block_table.shape[1], k_cache.shape[1],
+                                        k_cache.shape[0], _ptr(cu_seqlens), _ptr(kv_lens), num, total, int(max_q_len),
+                                        _ptr(lse), _ptr(weights), weights.shape[2], Hq, Hkv, D,
+                                        float(scale) if scale else 0.0, bool(causal), dt, _stream(None))
+    _check(st, "fa_paged_key_weights")
+    return weights
+
+
+def fa_paged_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                   weights: torch.Tensor, budget: int, recent: int,
+                   stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Cuts every sequence and key head to `budget` keys: the last `recent` and, of the others, those
+    of most accumulated weight (B, Hkv, width). Rows are closed up in place, in their order. Returns
+    (kept int32 (B, Hkv, budget): old slots, then -1; new kv_lens; new weights)."""
+    Hkv, num = _paged_args(None, k_cache, v_cache, block_table, None, kv_lens)
+    _cuda_contig("weights", weights)
+    if weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[0] != num or weights.shape[1] != Hkv:
+        raise ValueError("weights must be float32 (sequences, Hkv, width)")
+    _same_device(k_cache, weights)
+    dt = _dtype_code(k_cache)
+    with _on_stream(k_cache, stream):
+        kept = torch.empty((num, Hkv, max(0, int(budget))), dtype=torch.int32, device=k_cache.device)
+        new_lens = torch.empty_like(kv_lens)
+        new_weights = torch.empty_like(weights)
+        st = lib().fa_paged_evict(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], k_cache.shape[1],
+                                  k_cache.shape[0], _ptr(kv_lens), _ptr(weights), weights.shape[2], int(budget), int(recent),
+                                  _ptr(kept), _ptr(new_lens), _ptr(new_weights), num, Hkv, k_cache.shape[3], dt,
+                                  _stream(None))
+    _check(st, "fa_paged_evict")
+    return kept, new_lens, new_weights
 
 
 def fa_device_status(stream=None, device=None) -> Tuple[int, int]:

@@ -88,6 +88,19 @@ bool encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64
     return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+namespace fa {
+uint64_t host_wait_limit_ns() { return wait_limit_ns(); }
+int host_sm_count() { return sm_count(); }
+bool host_head_dim_ok(int D) { return head_dim_ok(D); }
+bool host_encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows) {
+    return encode_map(m, base, bf16, D, H, N, inner, rows);
+}
+}  // namespace fa
+
+namespace {
+
 struct Paging {
     const int32_t *block_table;
     int max_blocks, page_size, num_pages;
@@ -273,7 +286,7 @@ bool bwd_aligned(const void *q, const void *k, const void *v, const void *out, c
 
 // The error words of the kernel families (one per compilation unit), read and cleared in one
 // launch on the caller's stream; the first nonzero code wins.
-constexpr int kErrorWords = 5;
+constexpr int kErrorWords = 9;
 struct ErrorWords {
     int *code[kErrorWords];
     int *where[kErrorWords];
@@ -426,7 +439,11 @@ fa_status fa_device_status(int *where, void *stream) {
         fa::fwd_paged_error_addrs(&w.code[1], &w.where[1]) != cudaSuccess ||
         fa::bwd_error_addrs(&w.code[2], &w.where[2]) != cudaSuccess ||
         fa::pad_error_addrs(&w.code[3], &w.where[3]) != cudaSuccess ||
-        fa::bwd256_error_addrs(&w.code[4], &w.where[4]) != cudaSuccess)
+        fa::bwd256_error_addrs(&w.code[4], &w.where[4]) != cudaSuccess ||
+        fa::qk_norm_error_addrs(&w.code[5], &w.where[5]) != cudaSuccess ||
+        fa::chunk_rows_error_addrs(&w.code[6], &w.where[6]) != cudaSuccess ||
+        fa::key_weights_error_addrs(&w.code[7], &w.where[7]) != cudaSuccess ||
+        fa::evict_error_addrs(&w.code[8], &w.where[8]) != cudaSuccess)
         return FA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     status_collect_kernel<<<1, 1, 0, st>>>(w);

@@ -7,6 +7,14 @@
 
 namespace fa {
 
+// Host helpers of fa_api.cu shared by the C-ABI sources: the bound of every wait, the current
+// device's SM count (-1: error), the supported head dims, and the TMA map of a token-major (N, H, D)
+// 16-bit tensor with boxes of `inner` elements of one head of `rows` tokens.
+uint64_t host_wait_limit_ns();
+int host_sm_count();
+bool host_head_dim_ok(int D);
+bool host_encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows);
+
 // Kernel parameters of the attention forward (passed by value).
 struct FwdParams {
     void *out;                  // token-major (N, H, D) output
@@ -98,6 +106,82 @@ cudaError_t bwd256_error_addrs(int **code, int **where);
 // memory that belongs to the library's module image; its address on the current device.
 constexpr int64_t kNoallocDeltaFloats = int64_t(1) << 24;
 cudaError_t noalloc_delta_buffer(float **ptr);
+
+// Norm of queries and keys with the position rotation (fa_qk_norm.cu).
+struct QkNormParams {
+    const void *q, *k, *v;                      // rows of tokens; v: paged form only
+    int64_t q_stride, k_stride, v_stride;       // elements from one token to the next
+    const void *wq, *wk;                        // D weights each (null: ones)
+    int w32;                                    // weights are float32 (else the type of q)
+    const float *cos_sin;                       // (max_pos, rot): rot/2 cosines, rot/2 sines
+    int64_t max_pos;
+    int rot;
+    const int64_t *positions;                   // (n); paged form: null takes the token's slot
+    void *q_out, *k_out, *v_out;                // paged form: k_out, v_out are the pools; backward: dq, dk
+    int64_t q_out_stride, k_out_stride;
+    const void *dq_out, *dk_out;                // backward: gradients of q_out, k_out
+    int64_t dq_out_stride, dk_out_stride;
+    float *partials, *dwq, *dwk;                // backward: (kQkNormBwdCtas, 2, D) workspace; weight gradients
+    int64_t n;                                  // tokens
+    int Hq, Hk;
+    float eps;
+    // paged form (cu_seqlens null otherwise)
+    const int32_t *cu_seqlens, *kv_lens, *block_table;
+    int num_seqs, max_blocks, page_shift, num_pages;
+    // set by the launcher
+    int heads_per_warp, q_units, k_units, units_per_token;
+};
+constexpr int kQkNormBwdCtas = 592;
+cudaError_t launch_qk_norm(int D, bool bf16, bool interleaved, bool backward, const QkNormParams &p, cudaStream_t st);
+cudaError_t qk_norm_error_addrs(int **code, int **where);
+
+// New tokens over a paged cache (fa_chunk.cuh).
+struct ChunkParams {
+    const void *q;                              // (total, Hq, D)
+    void *out;                                  // the same
+    float *lse;                                 // (Hq, total) or null
+    const float *lse_in;                        // key weights: the attention's LSE
+    float *weights;                             // key weights: (num_seqs, Hkv, width)
+    int64_t width;
+    const int32_t *cu_seqlens, *kv_lens, *block_table;
+    int num_seqs, total, max_blocks, page_shift, num_pages;
+    int capacity;                               // keys that a table row can name
+    int Hq, Hkv, G;                             // G = Hq / Hkv
+    float scale_log2;
+    uint64_t timeout_ns;
+    int min_steps;                              // least steps of a CTA's run
+    // workspace: per CTA (sequence, key head, row tile, pieces); per slot and row (m, l) and O
+    int4 *desc;
+    float2 *part_ml;
+    float *part_o;
+};
+constexpr int kChunkMaxCtas = 160;              // the workspace is laid out for this many CTAs
+// Tiles of 16 rows (fa_chunk_rows.cu).
+cudaError_t launch_chunk_rows(int D, bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const ChunkParams &p, int ctas, cudaStream_t st);
+int chunk_rows_tile();
+int chunk_rows_box(int D, int page_size);       // rows of a K or V box
+cudaError_t chunk_rows_error_addrs(int **code, int **where);
+// Weight received by each key (fa_key_weights.cu).
+cudaError_t launch_key_weights(int D, bool bf16, bool causal, const CUtensorMap &tk, const ChunkParams &p, int ctas,
+                               cudaStream_t st);
+int key_weights_box(int page_size);
+cudaError_t key_weights_error_addrs(int **code, int **where);
+
+// Eviction by accumulated weight (fa_evict.cu).
+struct EvictParams {
+    void *k_cache, *v_cache;
+    const int32_t *block_table, *kv_lens;
+    int batch, max_blocks, page_shift, num_pages, capacity;
+    int Hkv, D;
+    const float *weights;                       // (batch, Hkv, width)
+    int64_t width;
+    int budget, recent;
+    int32_t *kept, *new_lens;                   // (batch, Hkv, budget), (batch)
+    float *new_weights;                         // as weights
+};
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t st);
+cudaError_t evict_error_addrs(int **code, int **where);
 
 // Unpad / pad (row gather / scatter + zero fill).
 cudaError_t launch_unpad(const void *x, const int64_t *indices, int64_t nnz, int64_t total_rows,
