@@ -286,7 +286,7 @@ bool bwd_aligned(const void *q, const void *k, const void *v, const void *out, c
 
 // The error words of the kernel families (one per compilation unit), read and cleared in one
 // launch on the caller's stream; the first nonzero code wins.
-constexpr int kErrorWords = 9;
+constexpr int kErrorWords = 10;
 struct ErrorWords {
     int *code[kErrorWords];
     int *where[kErrorWords];
@@ -443,7 +443,8 @@ fa_status fa_device_status(int *where, void *stream) {
         fa::qk_norm_error_addrs(&w.code[5], &w.where[5]) != cudaSuccess ||
         fa::chunk_rows_error_addrs(&w.code[6], &w.where[6]) != cudaSuccess ||
         fa::key_weights_error_addrs(&w.code[7], &w.where[7]) != cudaSuccess ||
-        fa::evict_error_addrs(&w.code[8], &w.where[8]) != cudaSuccess)
+        fa::evict_error_addrs(&w.code[8], &w.where[8]) != cudaSuccess ||
+        fa::chunk_tile_error_addrs(&w.code[9], &w.where[9]) != cudaSuccess)
         return FA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     status_collect_kernel<<<1, 1, 0, st>>>(w);

@@ -52,8 +52,13 @@ fa_status done(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Rows of a work item's tile for a call whose sequences have up to max_q_len new tokens.
-int chunk_tile(int, int, int) { return fa::chunk_rows_tile(); }
+// Whether a call whose sequences have up to max_q_len new tokens runs in tiles of 16 rows.
+bool few_rows(int G, int max_q_len) { return static_cast<int64_t>(max_q_len) * G <= fa::chunk_rows_tile(); }
+
+// Rows of a work item's tile.
+int chunk_tile(int G, int D, int max_q_len) {
+    return few_rows(G, max_q_len) ? fa::chunk_rows_tile() : fa::chunk_tile_rows(D);
+}
 
 size_t chunk_bytes(int R, int D, size_t *ml, size_t *o) {
     const size_t slots = 2 * static_cast<size_t>(fa::kChunkMaxCtas) * R;
@@ -239,13 +244,19 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     const int ctas = chunk_ctas();
     if (ctas <= 0) return FA_ERR_CUDA;
     const bool bf16 = dtype == FA_BF16;
-    const int inner = fa::fwd_box_inner_elems(D), box = fa::chunk_rows_box(D, page_size);
+    const bool few = few_rows(p.G, max_q_len);
+    const int inner = fa::fwd_box_inner_elems(D);
+    const int k_box = few ? fa::chunk_rows_box(D, page_size) : fa::chunk_tile_k_box(D, page_size);
+    const int v_box = few ? fa::chunk_rows_box(D, page_size) : fa::chunk_tile_v_box(D, page_size);
+    p.min_steps = few ? 1 : 2;  // at least the cost of a step
     CUtensorMap tk, tv;
     const int64_t rows = static_cast<int64_t>(num_pages) * page_size;
-    if (!fa::host_encode_map(&tk, k_cache, bf16, D, Hkv, rows, inner, box) ||
-        !fa::host_encode_map(&tv, v_cache, bf16, D, Hkv, rows, inner, box))
+    if (!fa::host_encode_map(&tk, k_cache, bf16, D, Hkv, rows, inner, k_box) ||
+        !fa::host_encode_map(&tv, v_cache, bf16, D, Hkv, rows, inner, v_box))
         return FA_ERR_CUDA;
-    return done(fa::launch_chunk_rows(D, bf16, causal != 0, tk, tv, p, ctas, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return done(few ? fa::launch_chunk_rows(D, bf16, causal != 0, tk, tv, p, ctas, cs)
+                    : fa::launch_chunk_tile(D, bf16, causal != 0, tk, tv, p, ctas, cs));
 }
 
 fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t *block_table, int max_blocks_per_seq,

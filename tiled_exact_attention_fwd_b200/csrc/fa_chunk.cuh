@@ -9,7 +9,7 @@
 // are written too).
 //
 // Split. The steps of all items, in the order (sequence, key head, row tile, key tile), are cut
-// into equal runs, one per CTA, whatever items they fall into: a serving batch of one long and
+// into runs of equal cost, one per CTA, whatever items they fall into: a serving batch of one long and
 // many short sequences then keeps every SM busy to the end, and a single sequence's keys are read
 // by all of them. An item that falls into several runs leaves an unnormalised O with (m, l) for
 // each piece in the workspace; chunk_combine_kernel joins the pieces in the order of the keys
@@ -63,22 +63,27 @@ template <int R, int BN, bool CAUSAL>
 __device__ __forceinline__ int tile_steps(const ChunkParams &p, const ChunkSeq &s, int t) {
     return max(1, (tile_keys<R, CAUSAL>(p, s, t) + BN - 1) / BN);
 }
-// Steps of one key head of a sequence.
-template <int R, int BN, bool CAUSAL>
-__device__ __forceinline__ int64_t head_steps(const ChunkParams &p, const ChunkSeq &s) {
-    const int tiles = (s.rows + R - 1) / R;
-    if (tiles == 0) return 0;
-    if (!CAUSAL) return static_cast<int64_t>(tiles) * max(1, (s.kv + BN - 1) / BN);
-    int64_t sum = 0;
-    for (int t = 0; t < tiles; ++t) sum += tile_steps<R, BN, CAUSAL>(p, s, t);
-    return sum;
+// Cost of a step of tile t: 2 where the tile fills more than one 128-row MMA tile, else 1.
+template <int R>
+__device__ __forceinline__ int tile_weight(const ChunkSeq &s, int t) {
+    return (R > 128 && s.rows - t * R > 128) ? 2 : 1;
 }
 
-// Where a CTA's run begins, and its length in steps.
+// Where a CTA's run begins: the item in which cost `lo` falls, whose own steps begin at cost `pos`.
+// The run takes the steps that begin in [lo, hi); `per` is hi - lo of a whole run.
 struct ChunkStart {
-    int b, h, t, j;
-    int64_t left, per;  // this CTA's steps; steps of a whole run
+    int b, h, t;
+    int64_t pos, lo, hi, per;
 };
+
+// Cost of one key head of a sequence.
+template <int R, int BN, bool CAUSAL>
+__device__ __forceinline__ int64_t head_cost(const ChunkParams &p, const ChunkSeq &s) {
+    const int tiles = (s.rows + R - 1) / R;
+    int64_t sum = 0;
+    for (int t = 0; t < tiles; ++t) sum += tile_steps<R, BN, CAUSAL>(p, s, t) * tile_weight<R>(s, t);
+    return sum;
+}
 
 __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
@@ -98,7 +103,7 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int b = base + lane * PER + i;
-            cost[i] = b < p.num_seqs ? head_steps<R, BN, CAUSAL>(p, chunk_seq(p, b)) * p.Hkv : 0;
+            cost[i] = b < p.num_seqs ? head_cost<R, BN, CAUSAL>(p, chunk_seq(p, b)) * p.Hkv : 0;
             mine += cost[i];
         }
     };
@@ -112,7 +117,7 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
     if (per < p.min_steps) per = p.min_steps;
     const int64_t start = per * cta;
     if (start >= total) {
-        if (lane == 0) *out = ChunkStart{0, 0, 0, 0, 0, per};
+        if (lane == 0) *out = ChunkStart{0, 0, 0, 0, 0, 0, per};
         return;
     }
     int64_t before = 0;
@@ -131,13 +136,16 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
                 if (start >= at && start < at + cost[i]) {
                     const int b = base + lane * PER + i;
                     const ChunkSeq s = chunk_seq(p, b);
-                    int64_t rem = start - at;
                     const int64_t one = cost[i] / p.Hkv;
-                    const int h = static_cast<int>(rem / one);
-                    rem -= h * one;
+                    const int h = static_cast<int>((start - at) / one);
+                    int64_t pos = at + h * one;
                     int t = 0;
-                    for (int n; rem >= (n = tile_steps<R, BN, CAUSAL>(p, s, t)); ++t) rem -= n;
-                    *out = ChunkStart{b, h, t, static_cast<int>(rem), min(per, total - start), per};
+                    for (;; ++t) {
+                        const int64_t n = static_cast<int64_t>(tile_steps<R, BN, CAUSAL>(p, s, t)) * tile_weight<R>(s, t);
+                        if (start < pos + n) break;
+                        pos += n;
+                    }
+                    *out = ChunkStart{b, h, t, pos, start, min(start + per, total), per};
                 }
                 at += cost[i];
             }
@@ -150,31 +158,34 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
 template <int R, int BN, bool CAUSAL>
 struct ChunkWalk {
     ChunkSeq s;
-    int b, h, t, j0, j1, steps, keys, tiles, rows;  // rows: valid rows of the tile
-    int64_t left;
+    int b, h, t, j0, j1, steps, keys, tiles, rows, weight;  // rows: valid rows of the tile
+    int64_t pos, lo, hi;
     // false when the CTA has no work
     __device__ __forceinline__ bool begin(const ChunkParams &p, const ChunkStart &st) {
-        left = st.left;
-        if (left <= 0) return false;
+        lo = st.lo;
+        hi = st.hi;
+        if (lo >= hi) return false;
         b = st.b;
         h = st.h;
         t = st.t;
+        pos = st.pos;
         s = chunk_seq(p, b);
         tiles = (s.rows + R - 1) / R;
-        set(p, st.j);
-        return true;
+        set(p);
+        return j0 < steps || next(p);  // lo may fall behind the start of the item's last step
     }
-    __device__ __forceinline__ void set(const ChunkParams &p, int j) {
+    __device__ __forceinline__ void set(const ChunkParams &p) {
         keys = tile_keys<R, CAUSAL>(p, s, t);
         steps = max(1, (keys + BN - 1) / BN);
         rows = min(R, s.rows - t * R);
-        j0 = j;
-        j1 = static_cast<int>(min(static_cast<int64_t>(steps), j + left));
+        weight = tile_weight<R>(s, t);
+        j0 = static_cast<int>(max(int64_t(0), lo - pos + weight - 1) / weight);
+        j1 = static_cast<int>(min(static_cast<int64_t>(steps), (hi - pos + weight - 1) / weight));
     }
     // moves to the next item; false at the end of the run
     __device__ __forceinline__ bool next(const ChunkParams &p) {
-        left -= j1 - j0;
-        if (left <= 0) return false;
+        pos += static_cast<int64_t>(steps) * weight;
+        if (pos >= hi) return false;
         if (++t == tiles) {
             t = 0;
             if (++h == p.Hkv) {
@@ -186,14 +197,17 @@ struct ChunkWalk {
                 tiles = (s.rows + R - 1) / R;
             }
         }
-        set(p, 0);
+        set(p);
         return true;
     }
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
     // workspace slot of a piece that is not whole
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (j0 == 0 ? 1 : 0); }
-    // pieces of the item begun here
-    __device__ __forceinline__ int pieces(int64_t per) const { return 1 + static_cast<int>((steps - j1 + per - 1) / per); }
+    // pieces of the item begun here: runs up to the one in which its last step begins (a run is
+    // at least as long as a step, so none between is empty)
+    __device__ __forceinline__ int pieces(int64_t per) const {
+        return static_cast<int>((pos + static_cast<int64_t>(steps - 1) * weight) / per) - static_cast<int>(blockIdx.x) + 1;
+    }
 };
 
 // Cache row of key position pos (below the sequence's length) of sequence b. An entry outside the

@@ -1,0 +1,527 @@
+// fa_chunk_tile.cu -- attention of new tokens over a paged cache where a key head has many rows
+// (fa_fwd_paged_chunk; prompt chunks): tiles of 128 rows on the tensor core.
+//
+// Rows are (new token, query head of the group), so a tile of a call with shared key heads holds
+// 128 / G tokens and every K/V tile that is loaded serves all of them. A CTA walks its run of steps
+// (fa_chunk.cuh), each one 128-key tile against two 128-row tiles A and B (one at D = 256, where two
+// O accumulators do not fit in TMEM), with the roles of the dense forward:
+//   warps 0-3, 4-7  softmax of tile A, B: a thread per row; running maximum and sum in registers, P
+//                   16-bit into TMEM (over S, or into columns of its own at D <= 64 so that the next
+//                   S can be computed meanwhile), O rescaled in TMEM when the maximum grew by 2^8.
+//   warp 8          K/V tiles by TMA, a box per page piece, the lanes issuing side by side.
+//   warp 9          tcgen05.mma: S_t = Q_t K^T, O_t += P_t V, A and B in turn, so that the tensor core
+//                   works on one while the softmax of the other runs. Before an item's last PV it clears
+//                   the rows of V past the last key.
+//   warp 10         D <= 64: issues the PVs (warp 9 then the QKs only).
+//   warp 11         gathers the Q rows (any group size) with cp.async into the swizzled tiles once the
+//                   last item's QKs have read them.
+// Rows of a tile past the sequence's last are zeros in Q and are not stored; a softmax warp without
+// a row skips the exponentials. An item that the split cuts leaves O, m and l in the workspace.
+#include "fa_chunk.cuh"
+#include "fa_fwd_kernel.cuh"
+
+namespace fa {
+
+namespace {
+
+// Shared-memory map, TMEM columns and register split: those of the dense forward (Cfg); the barrier
+// area holds this kernel's barriers and the run's start.
+template <int D>
+struct TileCfg : Cfg<D> {
+    using B = Cfg<D>;
+    static constexpr int R = B::BM * B::MAXQ;
+    static constexpr int BARS = 2 + 2 + 2 * B::NS + 2 + 2 + 2 + 2 + 1;
+    static constexpr int OFF_START = B::OFF_BAR + BARS * 8;
+    static constexpr int OFF_TMEM = OFF_START + static_cast<int>(sizeof(ChunkStart));
+    static_assert(BARS * 8 + sizeof(ChunkStart) + 8 <= 512, "barrier area");
+    static_assert(OFF_TMEM + 8 + 1024 <= B::SMEM_BYTES, "shared memory");
+};
+
+template <int D, bool BF16, bool CAUSAL>
+__global__ void __launch_bounds__(TileCfg<D>::NUM_THREADS, 1)
+chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+    using C = TileCfg<D>;
+    using Walk = ChunkWalk<C::R, C::BN, CAUSAL>;
+    constexpr int BM = C::BM, BN = C::BN, SW = C::SW, NS = C::NS, U = C::UNITS;
+    constexpr bool SINGLE = C::MAXQ == 1, DEC = C::DECOUPLED;
+    constexpr int CPB = SW / 16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem + C::OFF_Q, *sKV = smem + C::OFF_KV;
+    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *q_free = q_full + 2, *kv_full = q_free + 2, *kv_empty = kv_full + NS, *s_full = kv_empty + NS;
+    uint64_t *p_full = s_full + 2, *pv_done = p_full + 2, *s_free = pv_done + 2, *drain = s_free + 2;
+    ChunkStart *start = reinterpret_cast<ChunkStart *>(smem + C::OFF_START);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_TMEM + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t lim = p.timeout_ns;
+    constexpr int W_TMA = C::WARP_TMA, W_MMA = C::WARP_MMA, W_PV = C::WARP_MMA + 1, W_Q = C::WARP_MMA + 2;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 32 * W_TMA) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 32);
+            mbar_init(&q_free[t], 1);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 128);
+            mbar_init(&pv_done[t], 1);
+            mbar_init(&s_free[t], 4);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&kv_full[s], 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        mbar_init(drain, DEC ? 2 : 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == W_MMA) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (warp == 0) chunk_locate<C::R, BN, CAUSAL>(p, blockIdx.x, gridDim.x, start);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= C::NUM_SOFTMAX_WARPS) {
+        if constexpr (C::SPLIT_REGS) regs_dec<C::regs_low(false)>();
+        Walk w;
+        if (warp == W_TMA) {
+            // ------------------------------------------------------------ K/V producer
+            bool bad = false, ok = true;
+            int u = 0;  // ring parts issued
+            const uint64_t pol = l2_policy_evict_last();
+            for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
+                for (int j = w.j0; ok && j < w.j1; ++j) {
+                    const int valid = min(BN, w.keys - j * BN);
+                    for (int part = 0; part < 2 * U; ++part, ++u) {
+                        const int stage = u % NS;
+                        if (u >= NS &&
+                            !__all_sync(0xffffffffu, wait_bounded(&kv_empty[stage], ((u / NS) - 1) & 1, abort_flag, lim, 750))) {
+                            ok = false;
+                            break;
+                        }
+                        // part of K_j: some column blocks of all rows; part of V_j: some rows of all blocks
+                        const bool is_v = part >= U;
+                        const int sub = is_v ? part - U : part;
+                        const int rows = is_v ? C::VROWS_PER_UNIT : BN, r0 = is_v ? sub * C::VROWS_PER_UNIT : 0;
+                        const int b0 = is_v ? 0 : sub * C::KBLK_PER_UNIT, nb = is_v ? C::NBLK : C::KBLK_PER_UNIT;
+                        const int box = min(1 << p.page_shift, rows), have = min(rows, valid - r0);
+                        const int boxes = have > 0 ? (have + box - 1) / box : 0;
+                        if (lane == 0) mbar_arrive_expect_tx(&kv_full[stage], boxes * box * nb * SW);
+                        __syncwarp();
+                        uint8_t *dst = sKV + stage * C::UNIT_BYTES;
+                        for (int i = lane; i < boxes * nb; i += 32) {
+                            const int bx = i / nb, blk = i - bx * nb;
+                            const int row = chunk_page_row(p, w.b, j * BN + r0 + bx * box, bad);
+                            tma_load_3d(dst + (blk * rows + bx * box) * SW, is_v ? &tm_v : &tm_k, &kv_full[stage],
+                                        (b0 + blk) * C::SWE, w.h, row, pol);
+                        }
+                    }
+                }
+            }
+            if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(FA_ERR_INDEX, 751);
+            if (*abort_flag) {  // the copies in flight land before the shared memory goes away
+                for (int v = max(0, u - NS); v < u; ++v) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(&kv_full[v % NS], (v / NS) & 1) && global_timer_ns() - t0 < lim) {
+                    }
+                }
+            }
+        } else if (warp == W_MMA || (DEC && warp == W_PV)) {
+            // ------------------------------------------------------------ MMA issuer(s)
+            bool ok = true;
+            int u0 = 0, nq[2] = {0, 0};
+            int ga = 0, gb = 0;  // running key steps of tiles A, B
+            auto wait = [&](uint64_t *bar, uint32_t ph, int where) {
+                if (ok) ok = __all_sync(0xffffffffu, wait_bounded(bar, ph, abort_flag, lim, where));
+                return ok;
+            };
+            // S_t = Q_t K_jj^T; `first`: the first tile to use this K, `last`: the last
+            auto qk = [&](int t, int jj, bool first, bool last, bool item_end) {
+                const int gs = (t ? gb : ga) + jj, buf = SINGLE ? (gs & 1) : t;
+                if (jj == 0) {
+                    if (!wait(&q_full[t], nq[t] & 1, 760 + t)) return;
+                    fence_proxy_async_smem();  // Q was written by cp.async
+                }
+                if (DEC && gs > 0 && !wait(&s_free[t], (gs - 1) & 1, 762 + t)) return;
+                tc_fence_after_sync();
+                constexpr uint32_t idesc = idesc_f16(BM, BN, BF16, false), dhi = smem_desc_hi(8 * SW, C::LAYOUT);
+                const uint32_t q_lo = smem_desc_lo(smem_u32(sQ + t * C::Q_BYTES), 16);
+                constexpr int UK = D / 16 / U;
+#pragma unroll
+                for (int un = 0; un < U; ++un) {
+                    const int part = u0 + 2 * jj * U + un, stage = part % NS;
+                    if (first) {
+                        if (!wait(&kv_full[stage], (part / NS) & 1, 764)) return;
+                        tc_fence_after_sync();
+                    }
+                    const uint32_t k_lo = smem_desc_lo(smem_u32(sKV + stage * C::UNIT_BYTES), 16);
+#pragma unroll
+                    for (int kk = 0; kk < UK; ++kk) {
+                        const int k = un * UK + kk;
+                        const uint32_t blk = (k * 32) / SW, off = (k * 32) % SW, lb = blk - un * C::KBLK_PER_UNIT;
+                        umma_ss_elect(tmem + buf * BN, q_lo + ((blk * BM * SW + off) >> 4), k_lo + ((lb * BN * SW + off) >> 4), dhi,
+                                      idesc, k > 0 ? 1u : 0u);
+                    }
+                    if (un + 1 == U) umma_commit_elect(&s_full[buf]);
+                    if (last) umma_commit_elect(&kv_empty[stage]);
+                }
+                if (item_end) umma_commit_elect(&q_free[t]);
+            };
+            // O_t += P_t V_jj; valid < BN: V_jj's rows from `valid` on are past the last key and are
+            // cleared first (what the page or the ring holds there may be NaN, and 0 NaN = NaN)
+            auto pv = [&](int t, int jj, bool first, bool last, int valid) {
+                const int gs = (t ? gb : ga) + jj, buf = SINGLE ? (gs & 1) : t;
+                const int part0 = u0 + (2 * jj + 1) * U;
+                if (first) {
+#pragma unroll
+                    for (int un = 0; un < U; ++un) {
+                        const int part = part0 + un, stage = part % NS;
+                        if (!wait(&kv_full[stage], (part / NS) & 1, 768)) return;
+                        if (valid >= BN) continue;
+                        const uint32_t dst = smem_u32(sKV + stage * C::UNIT_BYTES);
+                        const int r0 = max(0, valid - un * C::VROWS_PER_UNIT);
+                        constexpr int CPR = D / 8;  // whole swizzled rows: the order of their chunks does not matter
+                        for (int i = lane; i < (C::VROWS_PER_UNIT - r0) * CPR; i += 32) {
+                            const int r = r0 + i / CPR, ch = i % CPR;
+                            st_shared_v4(dst + (ch / CPB) * C::VROWS_PER_UNIT * SW + r * SW + (ch % CPB) * 16, 0u, 0u, 0u, 0u);
+                        }
+                    }
+                    if (valid < BN) {
+                        fence_proxy_async_smem();  // the zeros, before the tensor core reads them
+                        __syncwarp();
+                    }
+                }
+                if (!wait(&p_full[buf], (SINGLE ? (gs >> 1) : gs) & 1, 766 + t)) return;
+                tc_fence_after_sync();
+                constexpr uint32_t idesc = idesc_f16(BM, D, BF16, true), dhi = smem_desc_hi(8 * SW, C::LAYOUT);
+                const uint32_t a = tmem + (DEC ? C::P_COL + 64 * t : buf * BN), o = tmem + C::O_COL + t * D;
+                constexpr int UV = BN / 16 / U;
+#pragma unroll
+                for (int un = 0; un < U; ++un) {
+                    const int stage = (part0 + un) % NS;
+                    const uint32_t v_lo = smem_desc_lo(smem_u32(sKV + stage * C::UNIT_BYTES), C::VROWS_PER_UNIT * SW);
+#pragma unroll
+                    for (int kk = 0; kk < UV; ++kk) {
+                        const int k = un * UV + kk;
+                        umma_ts_elect(o, a + k * 8, v_lo + ((kk * 16 * SW) >> 4), dhi, idesc, (jj > 0 || k > 0) ? 1u : 0u);
+                    }
+                    if (un + 1 == U) umma_commit_elect(&pv_done[t]);
+                    if (last) umma_commit_elect(&kv_empty[stage]);
+                }
+            };
+            const bool do_qk = !DEC || warp == W_MMA, do_pv = !DEC || warp == W_PV;
+            for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
+                const int n = w.j1 - w.j0;
+                const bool two = !SINGLE && w.rows > BM;
+                const int end = w.keys - w.j0 * BN;  // keys of the segment (its last tile may reach past them)
+                auto valid = [&](int jj) { return max(0, end - jj * BN); };
+                if (SINGLE) {
+                    for (int i = 0; ok && i < 2 * n; ++i) {
+                        bool is_v;
+                        int j;
+                        decode_step(i, n, is_v, j);
+                        if (is_v) pv(0, j, true, true, valid(j));
+                        else qk(0, j, true, true, j == n - 1);
+                    }
+                } else {
+                    // A and B in turn; separate P buffers: a QK runs one step ahead of the PVs
+                    if (do_qk) qk(0, 0, true, !two, n == 1);
+                    if (do_qk && ok && two) qk(1, 0, false, true, n == 1);
+                    for (int j = 1; ok && j <= n; ++j) {
+                        if (DEC) {
+                            if (do_qk && j < n) qk(0, j, true, !two, j == n - 1);
+                            if (do_qk && ok && two && j < n) qk(1, j, false, true, j == n - 1);
+                            if (do_pv) pv(0, j - 1, true, !two, valid(j - 1));
+                            if (do_pv && ok && two) pv(1, j - 1, false, true, BN);
+                        } else {
+                            pv(0, j - 1, true, !two, valid(j - 1));
+                            if (ok && j < n) qk(0, j, true, !two, j == n - 1);
+                            if (ok && two) pv(1, j - 1, false, true, BN);
+                            if (ok && two && j < n) qk(1, j, false, true, j == n - 1);
+                        }
+                    }
+                }
+                u0 += 2 * U * n;
+                ga += n;
+                nq[0]++;
+                if (two) {
+                    gb += n;
+                    nq[1]++;
+                }
+            }
+            umma_commit_elect(drain);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < lim) {
+            }
+        } else if (warp == W_Q) {
+            // ------------------------------------------------------------ Q rows
+            bool ok = true;
+            int nq[2] = {0, 0};
+            auto wait = [&](uint64_t *bar, uint32_t ph, int where) {
+                if (ok) ok = __all_sync(0xffffffffu, wait_bounded(bar, ph, abort_flag, lim, where));
+                return ok;
+            };
+            for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
+                const bool two = !SINGLE && w.rows > BM;
+                for (int t = 0; t < (two ? 2 : 1); ++t) {
+                    if (nq[t] > 0 && !wait(&q_free[t], (nq[t] - 1) & 1, 770 + t)) break;
+                    const uint32_t dst = smem_u32(sQ + t * C::Q_BYTES);
+                    for (int g = 0; g < BM; g += 32) {
+                        // this lane's row of the group: its place in q, or nowhere (zeros)
+                        const int pr = w.t * C::R + t * BM + g + lane;
+                        const bool there = pr < w.s.rows;
+                        const int i = there ? pr / p.G : 0;
+                        const int64_t at = (static_cast<int64_t>(w.s.q0 + i) * p.Hq + w.h * p.G + (there ? pr - i * p.G : 0)) * D;
+                        constexpr int CPR = D / 8;
+#pragma unroll 4
+                        for (int k = 0; k < CPR; ++k) {
+                            const int idx = k * 32 + lane, rr = idx / CPR, ch = idx % CPR, r = g + rr;
+                            const int64_t src = __shfl_sync(0xffffffffu, at, rr);
+                            const bool ok_row = __shfl_sync(0xffffffffu, there, rr);
+                            const int swz = SW == 128 ? (r & 7) : ((r >> 1) & 3);
+                            cp_async_16_zfill(dst + (ch / CPB) * BM * SW + r * SW + (((ch % CPB) ^ swz) << 4),
+                                              static_cast<const uint16_t *>(p.q) + src + ch * 8, ok_row ? 16u : 0u);
+                        }
+                    }
+                    cp_async_mbar_arrive(&q_full[t]);
+                    nq[t]++;
+                }
+            }
+            cp_async_wait_all();
+        }
+    } else {
+        // ------------------------------------------------------------ softmax + epilogue
+        if constexpr (C::SPLIT_REGS) regs_inc<C::regs_high(false)>();
+        const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t o_addr = tmem + lane_base + C::O_COL + t * D;
+        const float sc = p.scale_log2;
+        bool ok = true;
+        int gbase = 0;
+        int4 desc = make_int4(0, 0, 0, 0);
+        Walk w;
+#pragma unroll 1
+        for (bool more = w.begin(p, *start); more; more = w.next(p)) {
+            if (w.j0 == 0 && w.j1 < w.steps) desc = make_int4(w.b, w.h, w.t, w.pieces(start->per));
+            if (t == 1 && w.rows <= BM) continue;  // tile absent
+            const int n = w.j1 - w.j0;
+            const int pr = w.t * C::R + t * BM + r;
+            const bool row_ok = pr < w.s.rows;
+            const bool busy = w.t * C::R + t * BM + quarter * 32 < w.s.rows;  // this warp has a row
+            // keys this row sees, counted from the segment's first
+            int hi = (row_ok ? token_keys<CAUSAL>(w.s, pr / p.G) : w.keys) - w.j0 * BN;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int jj = 0; ok && jj < n; ++jj, hi -= BN) {
+                const int gs = gbase + jj, buf = SINGLE ? (gs & 1) : t;
+                const uint32_t ph = (SINGLE ? (gs >> 1) : gs) & 1;
+                if (!__all_sync(0xffffffffu, wait_bounded(&s_full[buf], ph, abort_flag, lim, 780 + t))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                if (!busy) {
+                    if (DEC && lane == 0) mbar_arrive(&s_free[t]);
+                    if ((SINGLE || DEC) && jj > 0 &&
+                        !__all_sync(0xffffffffu, wait_bounded(&pv_done[t], (gs - 1) & 1, abort_flag, lim, 782))) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive(&p_full[buf]);
+                    continue;
+                }
+                uint32_t sr[BN];
+#pragma unroll
+                for (int cc = 0; cc < BN / 32; ++cc) tmem_ld32(tmem + lane_base + buf * BN + cc * 32, sr + cc * 32);
+                tmem_ld_wait();
+                tmem_reg_fence<BN>(sr);
+                if (DEC) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[t]);
+                }
+                if (__any_sync(0xffffffffu, hi < BN)) {
+#pragma unroll
+                    for (int i = 0; i < BN; ++i)
+                        if (i >= hi) sr[i] = __float_as_uint(-INFINITY);
+                }
+                const float m_cand = row_max<BN>(sr) * sc;
+                const bool grow = m_cand > m + 8.0f;
+                float alpha = 1.f;
+                if (grow) {
+                    alpha = ex2_approx(m - m_cand);
+                    m = m_cand;
+                }
+                const bool warp_grow = __any_sync(0xffffffffu, grow);
+                const float neg_m = (m == -INFINITY) ? 0.f : -m;
+                auto rescale = [&]() {  // O holds the earlier tiles' sum: to the new running maximum
+                    const uint64_t a2 = f2(alpha, alpha);
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(o_addr + cc * 32, o);
+                        tmem_ld_wait();
+                        tmem_reg_fence<32>(o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x, y;
+                            f2_split(fmul2(f2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), a2), x, y);
+                            o[2 * i] = __float_as_uint(x);
+                            o[2 * i + 1] = __float_as_uint(y);
+                        }
+                        tmem_st32(o_addr + cc * 32, o);
+                    }
+                };
+                if constexpr (DEC) {
+                    uint32_t pk[BN / 2];
+                    const float rs = softmax_row_to_regs<BN, BF16>(sr, sc, neg_m, pk);
+                    l = fmaf(l, alpha, rs);
+                    if (jj > 0) {  // P's columns and O are free once the last PV is done
+                        if (!__all_sync(0xffffffffu, wait_bounded(&pv_done[t], (gs - 1) & 1, abort_flag, lim, 784))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        if (warp_grow) rescale();
+                    }
+#pragma unroll
+                    for (int cc = 0; cc < BN / 64; ++cc) tmem_st32(tmem + lane_base + C::P_COL + 64 * t + cc * 32, pk + cc * 32);
+                    tmem_st_wait();
+                } else {
+                    const float rs = softmax_chunk_store<BN, BF16>(sr, sc, neg_m, tmem + lane_base + buf * BN);
+                    l = fmaf(l, alpha, rs);
+                    tmem_st_wait();
+                    if (jj > 0) {
+                        // two tiles: PV_t(j - 1) was issued before QK_t(j), so s_full has shown it done
+                        if (SINGLE &&
+                            !__all_sync(0xffffffffu, wait_bounded(&pv_done[t], (gs - 1) & 1, abort_flag, lim, 786))) {
+                            ok = false;
+                            break;
+                        }
+                        if (warp_grow) {
+                            tc_fence_after_sync();
+                            rescale();
+                            tmem_st_wait();
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(&p_full[buf]);
+            }
+            if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&pv_done[t], (gbase + n - 1) & 1, abort_flag, lim, 788 + t));
+            gbase += n;
+            if (!ok || !busy) continue;
+            tc_fence_after_sync();
+            const bool whole = w.whole();
+            const int i = pr / p.G;
+            const int64_t tok = w.s.q0 + i;
+            const int head = w.h * p.G + pr - i * p.G;
+            const int64_t slot = static_cast<int64_t>(w.slot()) * C::R + t * BM + r;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D;
+            float *po = p.part_o + slot * D;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_addr + c0, o);
+                tmem_ld_wait();
+                tmem_reg_fence<32>(o);
+                if (row_ok) {
+                    if (whole) {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = pack2<BF16>(__uint_as_float(o[v * 8 + 2 * k]) * inv, __uint_as_float(o[v * 8 + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(out + c0 + v * 8) = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            *reinterpret_cast<uint4 *>(po + c0 + v * 4) = make_uint4(o[v * 4], o[v * 4 + 1], o[v * 4 + 2], o[v * 4 + 3]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (row_ok) {
+                if (!whole)
+                    p.part_ml[slot] = make_float2(m, l);
+                else if (p.lse)
+                    p.lse[static_cast<int64_t>(head) * p.total + tok] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+            }
+        }
+        if (threadIdx.x == 0) p.desc[blockIdx.x] = desc;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == W_MMA) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+template <int D, bool BF16, bool CAUSAL>
+cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p, int ctas, cudaStream_t st) {
+    using C = TileCfg<D>;
+    auto kern = chunk_tile_kernel<D, BF16, CAUSAL>;
+    static uint64_t attr_set_mask = 0;  // per device; setting it twice is harmless
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(__atomic_load_n(&attr_set_mask, __ATOMIC_ACQUIRE) & bit)) {
+        if (C::SPLIT_REGS) {
+            // the register split draws on the registers the CTA launches with
+            cudaFuncAttributes fa_attr;
+            e = cudaFuncGetAttributes(&fa_attr, kern);
+            if (e != cudaSuccess) return e;
+            if (fa_attr.numRegs * C::NUM_THREADS < 128 * C::regs_low(false) + 256 * C::regs_high(false))
+                return cudaErrorInvalidConfiguration;
+        }
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&attr_set_mask, bit, __ATOMIC_RELEASE);
+    }
+    kern<<<ctas, C::NUM_THREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_combine<D, BF16>(p, C::R, ctas, st);
+}
+
+template <int D>
+cudaError_t launch_d(bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p, int ctas,
+                     cudaStream_t st) {
+    if (bf16) return causal ? launch<D, true, true>(tk, tv, p, ctas, st) : launch<D, true, false>(tk, tv, p, ctas, st);
+    return causal ? launch<D, false, true>(tk, tv, p, ctas, st) : launch<D, false, false>(tk, tv, p, ctas, st);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tile(int D, bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const ChunkParams &p, int ctas, cudaStream_t st) {
+    switch (D) {
+        case 32: return launch_d<32>(bf16, causal, tk, tv, p, ctas, st);
+        case 64: return launch_d<64>(bf16, causal, tk, tv, p, ctas, st);
+        case 128: return launch_d<128>(bf16, causal, tk, tv, p, ctas, st);
+        case 256: return launch_d<256>(bf16, causal, tk, tv, p, ctas, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+int chunk_tile_rows(int D) { return D == 256 ? 128 : 256; }
+int chunk_tile_k_box(int, int page_size) { return page_size < 128 ? page_size : 128; }
+int chunk_tile_v_box(int D, int page_size) {
+    const int rows = D == 256 ? 64 : 128;
+    return page_size < rows ? page_size : rows;
+}
+
+cudaError_t chunk_tile_error_addrs(int **code, int **where) { return device_error_addrs(code, where); }
+
+}  // namespace fa

@@ -162,6 +162,13 @@ cudaError_t launch_chunk_rows(int D, bool bf16, bool causal, const CUtensorMap &
 int chunk_rows_tile();
 int chunk_rows_box(int D, int page_size);       // rows of a K or V box
 cudaError_t chunk_rows_error_addrs(int **code, int **where);
+// Tiles of 128 rows on the tensor core, two at a time at D <= 128 (fa_chunk_tile.cu).
+cudaError_t launch_chunk_tile(int D, bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const ChunkParams &p, int ctas, cudaStream_t st);
+int chunk_tile_rows(int D);
+int chunk_tile_k_box(int D, int page_size);
+int chunk_tile_v_box(int D, int page_size);
+cudaError_t chunk_tile_error_addrs(int **code, int **where);
 // Weight received by each key (fa_key_weights.cu).
 cudaError_t launch_key_weights(int D, bool bf16, bool causal, const CUtensorMap &tk, const ChunkParams &p, int ctas,
                                cudaStream_t st);

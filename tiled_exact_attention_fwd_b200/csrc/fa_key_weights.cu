@@ -29,6 +29,11 @@ __device__ __forceinline__ int first_tile(const ChunkParams &p, const ChunkSeq &
     return max(0, j * BN - (s.kv - s.n)) * p.G / R;  // token i sees key j * BN when i >= j * BN - (kv - n)
 }
 
+struct KeyStart {
+    int b, h, j;
+    int64_t left;
+};
+
 // A walk over key tiles: (sequence, key head, key tile), each with the row tiles [t0, tiles).
 template <int R, int BN, bool CAUSAL>
 struct KeyWalk {
@@ -49,7 +54,7 @@ struct KeyWalk {
         tiles = (s.rows + R - 1) / R;
     }
     // one warp: where run `cta` begins (st->j: key tile); a run takes the items that begin in it
-    __device__ static void locate(const ChunkParams &p, int cta, int ctas, ChunkStart *st) {
+    __device__ static void locate(const ChunkParams &p, int cta, int ctas, KeyStart *st) {
         constexpr int PER = 4;
         const int lane = threadIdx.x & 31;
         int64_t cost[PER], total = 0, mine = 0;
@@ -69,7 +74,7 @@ struct KeyWalk {
         if (cta == 0)
             for (int b = lane; b < p.num_seqs; b += 32) chunk_check(p, b);
         const int64_t per = (total + ctas - 1) / ctas, start = per * cta;
-        if (lane == 0) *st = ChunkStart{0, 0, 0, 0, 0, per};
+        if (lane == 0) *st = KeyStart{0, 0, 0, 0};
         __syncwarp();
         if (start >= total) return;
         int64_t before = 0;
@@ -102,7 +107,7 @@ struct KeyWalk {
                         }
                         const int64_t skipped = sum - rem;  // steps of the run that belong to an item begun before it
                         const int64_t left = min(per, total - start) - skipped;
-                        *st = ChunkStart{b, h, 0, j, left, per};
+                        *st = KeyStart{b, h, j, left};
                     }
                     at += cost[i];
                 }
@@ -110,7 +115,7 @@ struct KeyWalk {
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
-    __device__ __forceinline__ bool begin(const ChunkParams &p, const ChunkStart &st) {
+    __device__ __forceinline__ bool begin(const ChunkParams &p, const KeyStart &st) {
         left = st.left;
         if (left <= 0) return false;
         b = st.b;
@@ -151,7 +156,7 @@ struct KeyCfg {
     static constexpr int NS = STAGE >= 65536 ? 3 : (STAGE >= 32768 ? 6 : 8);
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int OFF_START = OFF_BAR + 2 * NS * 8;
-    static constexpr int OFF_ABORT = OFF_START + static_cast<int>(sizeof(ChunkStart));
+    static constexpr int OFF_ABORT = OFF_START + static_cast<int>(sizeof(KeyStart));
     static constexpr int SMEM = OFF_ABORT + 16 + 1024;
     static constexpr int THREADS = 32 * (NW + 1);
 };
@@ -165,7 +170,7 @@ key_weights_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const ChunkPar
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR), *empty = full + NS;
-    ChunkStart *start = reinterpret_cast<ChunkStart *>(smem + C::OFF_START);
+    KeyStart *start = reinterpret_cast<KeyStart *>(smem + C::OFF_START);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_ABORT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == C::NW * 32) {
@@ -179,7 +184,7 @@ key_weights_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const ChunkPar
     }
     if (warp == 0) Walk::locate(p, blockIdx.x, gridDim.x, start);
     __syncthreads();
-    const ChunkStart st = *start;
+    const KeyStart st = *start;
     if (warp == C::NW) {
         Walk w;
         bool bad = false;
