@@ -326,7 +326,7 @@ FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const vo
  *                time) need one each.
  * Offsets and lengths that do not fit total or the table are cut to it, and FA_ERR_INDEX is left for
  * fa_device_status; the same for a table entry outside the pool, where page 0 is read instead.
- * total * Hq / Hkv < 2^31. total == 0 or num_seqs == 0 is a successful no-op.
+ * total * Hq / Hkv < 2^30, Hq / Hkv <= 128. total == 0 or num_seqs == 0 is a successful no-op.
  */
 FA_API int64_t fa_fwd_paged_chunk_workspace(int Hq, int Hkv, int D, int max_q_len);
 FA_API fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_cache,

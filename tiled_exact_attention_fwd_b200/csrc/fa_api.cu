@@ -97,6 +97,21 @@ bool host_head_dim_ok(int D) { return head_dim_ok(D); }
 bool host_encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows) {
     return encode_map(m, base, bf16, D, H, N, inner, rows);
 }
+bool host_encode_group_map(CUtensorMap *m, const void *base, bool bf16, int D, int G, int Hkv, int64_t N, int inner,
+                           int tokens) {
+    EncodeTiledFn f = encode_fn();
+    if (!f) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(D) * 2, group = row * G, token = group * Hkv;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(Hkv),
+                                static_cast<cuuint64_t>(N)};
+    const cuuint64_t strides[3] = {row, group, token};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapSwizzle sw = (inner * 2 == 128) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    return f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace fa
 
 namespace {

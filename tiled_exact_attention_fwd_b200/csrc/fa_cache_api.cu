@@ -31,7 +31,8 @@ int capacity_of(int max_blocks, int page_size) {
     return c > INT32_MAX ? INT32_MAX : static_cast<int>(c);
 }
 
-bool heads_ok(int Hq, int Hkv) { return Hq > 0 && Hkv > 0 && Hq % Hkv == 0; }
+// Up to 128 query heads share a key head (a token's rows lie in one MMA tile).
+bool heads_ok(int Hq, int Hkv) { return Hq > 0 && Hkv > 0 && Hq % Hkv == 0 && Hq / Hkv <= 128; }
 
 // Checks shared by the three norm entry points.
 fa_status norm_check(const void *q, const void *k, const float *cos_sin, int64_t max_pos, int rot, int64_t n, int Hq, int Hk,
@@ -53,7 +54,9 @@ fa_status done(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Whether a call whose sequences have up to max_q_len new tokens runs in tiles of 16 rows.
-bool few_rows(int G, int max_q_len) { return static_cast<int64_t>(max_q_len) * G <= fa::chunk_rows_tile(); }
+bool few_rows(int G, int max_q_len) {
+    return G <= fa::chunk_rows_tile() && static_cast<int64_t>(max_q_len) * G <= fa::chunk_rows_tile();
+}
 
 // Rows of a work item's tile.
 int chunk_tile(int G, int D, int max_q_len) {
@@ -62,7 +65,7 @@ int chunk_tile(int G, int D, int max_q_len) {
 
 size_t chunk_bytes(int R, int D, size_t *ml, size_t *o) {
     const size_t slots = 2 * static_cast<size_t>(fa::kChunkMaxCtas) * R;
-    *ml = round256(fa::kChunkMaxCtas * sizeof(int4));
+    *ml = round256(fa::kChunkMaxCtas * sizeof(fa::ChunkDesc));
     *o = *ml + round256(slots * sizeof(float2));
     return *o + slots * D * sizeof(float);
 }
@@ -89,7 +92,6 @@ fa_status chunk_params(fa::ChunkParams &p, const void *q, const int32_t *block_t
     if (!(scale > 0.f)) scale = 1.0f / sqrtf(static_cast<float>(D));
     p.scale_log2 = scale * 1.4426950408889634f;
     p.timeout_ns = fa::host_wait_limit_ns();
-    p.min_steps = 1;
     return FA_OK;
 }
 
@@ -98,7 +100,7 @@ fa_status chunk_check(int max_blocks, int page_size, int num_pages, int num_seqs
     if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_DTYPE;
     if (!fa::host_head_dim_ok(D)) return FA_ERR_HEADDIM;
     if (!heads_ok(Hq, Hkv) || Hq > 65536 || num_seqs < 0 || total < 0 || max_q_len < 0) return FA_ERR_SHAPE;
-    if (static_cast<int64_t>(total) * (Hq / Hkv) > INT32_MAX) return FA_ERR_SHAPE;
+    if (static_cast<int64_t>(total) * (Hq / Hkv) > INT32_MAX / 2) return FA_ERR_SHAPE;
     return pages_ok(max_blocks, page_size, num_pages) ? FA_OK : FA_ERR_SHAPE;
 }
 
@@ -238,7 +240,7 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     size_t ml, o;
     chunk_bytes(R, D, &ml, &o);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.desc = reinterpret_cast<int4 *>(ws);
+    p.desc = reinterpret_cast<fa::ChunkDesc *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(ws + ml);
     p.part_o = reinterpret_cast<float *>(ws + o);
     const int ctas = chunk_ctas();
@@ -248,15 +250,20 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     const int inner = fa::fwd_box_inner_elems(D);
     const int k_box = few ? fa::chunk_rows_box(D, page_size) : fa::chunk_tile_k_box(D, page_size);
     const int v_box = few ? fa::chunk_rows_box(D, page_size) : fa::chunk_tile_v_box(D, page_size);
-    p.min_steps = few ? 1 : 2;  // at least the cost of a step
+    p.mma_tiles = few ? 1 : R / 128;
+    p.tile_tokens = p.mma_tiles * ((few ? R : 128) / p.G);
+    p.min_cost = p.mma_tiles;  // at least the cost of a step
+    p.out_align32 = aligned(out, 32);
     CUtensorMap tk, tv;
     const int64_t rows = static_cast<int64_t>(num_pages) * page_size;
     if (!fa::host_encode_map(&tk, k_cache, bf16, D, Hkv, rows, inner, k_box) ||
         !fa::host_encode_map(&tv, v_cache, bf16, D, Hkv, rows, inner, v_box))
         return FA_ERR_CUDA;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    return done(few ? fa::launch_chunk_rows(D, bf16, causal != 0, tk, tv, p, ctas, cs)
-                    : fa::launch_chunk_tile(D, bf16, causal != 0, tk, tv, p, ctas, cs));
+    if (few) return done(fa::launch_chunk_rows(D, bf16, causal != 0, tk, tv, p, ctas, cs));
+    CUtensorMap tq;
+    if (!fa::host_encode_group_map(&tq, q, bf16, D, p.G, Hkv, total, inner, 128 / p.G)) return FA_ERR_CUDA;
+    return done(fa::launch_chunk_tile(D, bf16, causal != 0, tq, tk, tv, p, ctas, cs));
 }
 
 fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t *block_table, int max_blocks_per_seq,

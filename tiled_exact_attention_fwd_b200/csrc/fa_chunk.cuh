@@ -3,19 +3,21 @@
 // of partial rows.
 //
 // Rows. A key head serves G query heads, so the G * n (new token, query head) pairs of a sequence
-// and key head are the rows that read the same K and V: row r is token r / G, head r % G of the
-// group. Rows go in tiles of R; a work item is (sequence, key head, row tile), and its steps are
-// the key tiles of BN keys that its last row sees (at least one, so that rows that see nothing
-// are written too).
+// and key head are the rows that read the same K and V. Rows go in tiles of T = R / G whole tokens
+// (at most R rows; row r is token r / G of the tile, head r % G of the group), so that a tile's Q is
+// one box in memory; a work item is (sequence, key head, row tile), and its steps are the key tiles
+// of BN keys that its last token sees (at least one, so that rows that see nothing are written
+// too).
 //
 // Split. The steps of all items, in the order (sequence, key head, row tile, key tile), are cut
-// into runs of equal cost, one per CTA, whatever items they fall into: a serving batch of one long and
-// many short sequences then keeps every SM busy to the end, and a single sequence's keys are read
+// into runs of equal cost, one per CTA, whatever items they fall into: a serving batch of one long
+// and many short sequences then keeps every SM busy to the end, and a single sequence's keys are read
 // by all of them. An item that falls into several runs leaves an unnormalised O with (m, l) for
 // each piece in the workspace; chunk_combine_kernel joins the pieces in the order of the keys
 // (fixed, so the same call gives the same bits). A CTA has at most two such pieces: the end of an
 // item begun by an earlier CTA (slot 2 c) and the beginning of one that a later CTA finishes
-// (slot 2 c + 1).
+// (slot 2 c + 1). Pieces lie column by column, [slot][D][R]: the writers hold a row per thread, so
+// a store of one column is a run of consecutive floats.
 #pragma once
 #include <cuda_runtime.h>
 #include <math.h>
@@ -28,7 +30,7 @@
 namespace fa {
 
 struct ChunkSeq {
-    int q0, n, rows, kv;  // first token row, new tokens, n * G, keys in the cache
+    int q0, n, kv;  // first token row, new tokens, keys in the cache
 };
 
 // Sequence b; offsets and lengths outside the tensors or the table are cut to them.
@@ -37,7 +39,6 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams &p, int b) {
     const int c0 = __ldg(p.cu_seqlens + b), c1 = __ldg(p.cu_seqlens + b + 1), kv = __ldg(p.kv_lens + b);
     s.q0 = min(max(c0, 0), p.total);
     s.n = max(min(c1, p.total) - s.q0, 0);
-    s.rows = s.n * p.G;
     s.kv = min(max(kv, 0), p.capacity);
     return s;
 }
@@ -54,19 +55,28 @@ __device__ __forceinline__ int token_keys(const ChunkSeq &s, int i) {
     return CAUSAL ? max(0, s.kv - s.n + i + 1) : s.kv;
 }
 
-// Keys that the last row of tile t sees, and the tile's steps.
-template <int R, bool CAUSAL>
-__device__ __forceinline__ int tile_keys(const ChunkParams &p, const ChunkSeq &s, int t) {
-    return token_keys<CAUSAL>(s, (min((t + 1) * R, s.rows) - 1) / p.G);
+// Keys that the last of the tokens before `end` sees, and the steps of the tile that ends there.
+template <bool CAUSAL>
+__device__ __forceinline__ int tile_keys(const ChunkSeq &s, int end) {
+    return token_keys<CAUSAL>(s, min(end, s.n) - 1);
 }
-template <int R, int BN, bool CAUSAL>
-__device__ __forceinline__ int tile_steps(const ChunkParams &p, const ChunkSeq &s, int t) {
-    return max(1, (tile_keys<R, CAUSAL>(p, s, t) + BN - 1) / BN);
+template <int BN, bool CAUSAL>
+__device__ __forceinline__ int tile_steps(const ChunkSeq &s, int end) {
+    return max(1, (tile_keys<CAUSAL>(s, end) + BN - 1) / BN);
 }
-// Cost of a step of tile t: 2 where the tile fills more than one 128-row MMA tile, else 1.
-template <int R>
-__device__ __forceinline__ int tile_weight(const ChunkSeq &s, int t) {
-    return (R > 128 && s.rows - t * R > 128) ? 2 : 1;
+// log2 of the cost of a step of the tile of T tokens that begins at token i: a step that fills two
+// MMA tiles (TILES = 2, T / 2 tokens each) costs twice as much as one that fills one.
+template <int TILES>
+__device__ __forceinline__ int step_shift(const ChunkSeq &s, int T, int i) {
+    return (TILES == 2 && s.n - i > (T >> 1)) ? 1 : 0;
+}
+
+// a / b for a, b >= 0 (b > 0), in 32 bits where they fit (they nearly always do, and a 64-bit
+// division is a long subroutine).
+__device__ __forceinline__ int64_t div_up_or_down(int64_t a, int64_t b, bool up) {
+    if (up) a += b - 1;
+    if ((a | b) >> 32 == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
 }
 
 // Where a CTA's run begins: the item in which cost `lo` falls, whose own steps begin at cost `pos`.
@@ -77,11 +87,10 @@ struct ChunkStart {
 };
 
 // Cost of one key head of a sequence.
-template <int R, int BN, bool CAUSAL>
-__device__ __forceinline__ int64_t head_cost(const ChunkParams &p, const ChunkSeq &s) {
-    const int tiles = (s.rows + R - 1) / R;
+template <int TILES, int BN, bool CAUSAL>
+__device__ __forceinline__ int64_t head_cost(const ChunkSeq &s, int T) {
     int64_t sum = 0;
-    for (int t = 0; t < tiles; ++t) sum += tile_steps<R, BN, CAUSAL>(p, s, t) * tile_weight<R>(s, t);
+    for (int i = 0; i < s.n; i += T) sum += tile_steps<BN, CAUSAL>(s, i + T) << step_shift<TILES>(s, T, i);
     return sum;
 }
 
@@ -93,17 +102,20 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 
 // One warp finds CTA cta's run (out: shared memory, written by one lane). Each lane takes four
 // consecutive sequences at a time, so up to 128 sequences cost one round of loads.
-template <int R, int BN, bool CAUSAL>
+template <int TILES, int BN, bool CAUSAL>
 __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int ctas, ChunkStart *out) {
     constexpr int PER = 4;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, T = p.tile_tokens;
     int64_t cost[PER], total = 0, mine = 0;
     auto costs = [&](int base) {
         mine = 0;
+        ChunkSeq s[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s[i] = chunk_seq(p, min(base + lane * PER + i, p.num_seqs - 1));
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int b = base + lane * PER + i;
-            cost[i] = b < p.num_seqs ? head_cost<R, BN, CAUSAL>(p, chunk_seq(p, b)) * p.Hkv : 0;
+            if (base + lane * PER + i >= p.num_seqs) s[i].n = 0;
+            cost[i] = head_cost<TILES, BN, CAUSAL>(s[i], T) * p.Hkv;
             mine += cost[i];
         }
     };
@@ -113,8 +125,8 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
     }
     if (cta == 0)
         for (int b = lane; b < p.num_seqs; b += 32) chunk_check(p, b);
-    int64_t per = (total + ctas - 1) / ctas;
-    if (per < p.min_steps) per = p.min_steps;
+    int64_t per = div_up_or_down(total, ctas, true);
+    if (per < p.min_cost) per = p.min_cost;
     const int64_t start = per * cta;
     if (start >= total) {
         if (lane == 0) *out = ChunkStart{0, 0, 0, 0, 0, 0, per};
@@ -129,36 +141,39 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
             const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        int64_t at = before + incl - mine;  // steps before this lane's sequences
+        int64_t at = before + incl - mine;  // cost before this lane's sequences
         if (start >= at && start < at + mine) {
+            int b = base + lane * PER;
+            int64_t mine_b = cost[0];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (start >= at && start < at + cost[i]) {
-                    const int b = base + lane * PER + i;
-                    const ChunkSeq s = chunk_seq(p, b);
-                    const int64_t one = cost[i] / p.Hkv;
-                    const int h = static_cast<int>((start - at) / one);
-                    int64_t pos = at + h * one;
-                    int t = 0;
-                    for (;; ++t) {
-                        const int64_t n = static_cast<int64_t>(tile_steps<R, BN, CAUSAL>(p, s, t)) * tile_weight<R>(s, t);
-                        if (start < pos + n) break;
-                        pos += n;
-                    }
-                    *out = ChunkStart{b, h, t, pos, start, min(start + per, total), per};
+            for (int i = 1; i < PER; ++i)
+                if (start >= at + mine_b) {
+                    at += mine_b;
+                    mine_b = cost[i];
+                    b = base + lane * PER + i;
                 }
-                at += cost[i];
+            const ChunkSeq s = chunk_seq(p, b);
+            const int64_t one = div_up_or_down(mine_b, p.Hkv, false);
+            const int64_t h = div_up_or_down(start - at, one, false);
+            int64_t pos = at + h * one;
+            int t = 0;
+            for (int i = 0;; i += T, ++t) {
+                const int64_t n = static_cast<int64_t>(tile_steps<BN, CAUSAL>(s, i + T)) << step_shift<TILES>(s, T, i);
+                if (start < pos + n) break;
+                pos += n;
             }
+            *out = ChunkStart{b, static_cast<int>(h), t, pos, start, min(start + per, total), per};
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
 }
 
-// A role's walk over its CTA's run: item after item, each the key tiles [j0, j1) of one row tile.
-template <int R, int BN, bool CAUSAL>
+// A role's walk over its CTA's run: item after item, each the key tiles [j0, j1) of one row tile
+// (tokens [i0, i0 + tokens) of the sequence).
+template <int TILES, int BN, bool CAUSAL>
 struct ChunkWalk {
     ChunkSeq s;
-    int b, h, t, j0, j1, steps, keys, tiles, rows, weight;  // rows: valid rows of the tile
+    int b, h, i0, j0, j1, steps, keys, tokens, shift;
     int64_t pos, lo, hi;
     // false when the CTA has no work
     __device__ __forceinline__ bool begin(const ChunkParams &p, const ChunkStart &st) {
@@ -167,34 +182,34 @@ struct ChunkWalk {
         if (lo >= hi) return false;
         b = st.b;
         h = st.h;
-        t = st.t;
+        i0 = st.t * p.tile_tokens;
         pos = st.pos;
         s = chunk_seq(p, b);
-        tiles = (s.rows + R - 1) / R;
         set(p);
         return j0 < steps || next(p);  // lo may fall behind the start of the item's last step
     }
     __device__ __forceinline__ void set(const ChunkParams &p) {
-        keys = tile_keys<R, CAUSAL>(p, s, t);
+        keys = tile_keys<CAUSAL>(s, i0 + p.tile_tokens);
         steps = max(1, (keys + BN - 1) / BN);
-        rows = min(R, s.rows - t * R);
-        weight = tile_weight<R>(s, t);
-        j0 = static_cast<int>(max(int64_t(0), lo - pos + weight - 1) / weight);
-        j1 = static_cast<int>(min(static_cast<int64_t>(steps), (hi - pos + weight - 1) / weight));
+        tokens = min(p.tile_tokens, s.n - i0);
+        shift = step_shift<TILES>(s, p.tile_tokens, i0);
+        const int64_t round = (1 << shift) - 1;
+        j0 = static_cast<int>(max(int64_t(0), lo - pos + round) >> shift);
+        j1 = static_cast<int>(min(static_cast<int64_t>(steps), (hi - pos + round) >> shift));
     }
     // moves to the next item; false at the end of the run
     __device__ __forceinline__ bool next(const ChunkParams &p) {
-        pos += static_cast<int64_t>(steps) * weight;
+        pos += static_cast<int64_t>(steps) << shift;
         if (pos >= hi) return false;
-        if (++t == tiles) {
-            t = 0;
+        i0 += p.tile_tokens;
+        if (i0 >= s.n) {
+            i0 = 0;
             if (++h == p.Hkv) {
                 h = 0;
                 do {
                     if (++b >= p.num_seqs) return false;
                     s = chunk_seq(p, b);
-                } while (s.rows == 0);
-                tiles = (s.rows + R - 1) / R;
+                } while (s.n == 0);
             }
         }
         set(p);
@@ -203,10 +218,12 @@ struct ChunkWalk {
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
     // workspace slot of a piece that is not whole
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (j0 == 0 ? 1 : 0); }
-    // pieces of the item begun here: runs up to the one in which its last step begins (a run is
-    // at least as long as a step, so none between is empty)
-    __device__ __forceinline__ int pieces(int64_t per) const {
-        return static_cast<int>((pos + static_cast<int64_t>(steps - 1) * weight) / per) - static_cast<int>(blockIdx.x) + 1;
+    // The item begun here, for the joining: its pieces run up to the CTA in whose run its last step
+    // begins (a run is at least as long as a step, so none between is empty).
+    __device__ __forceinline__ ChunkDesc desc(const ChunkParams &p, int64_t per) const {
+        const int64_t last = pos + (static_cast<int64_t>(steps - 1) << shift);
+        return ChunkDesc{static_cast<int>(div_up_or_down(last, per, false)) - static_cast<int>(blockIdx.x) + 1, s.q0 + i0,
+                         tokens, h * p.G};
     }
 };
 
@@ -224,69 +241,86 @@ __device__ __forceinline__ int chunk_page_row(const ChunkParams &p, int b, int p
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Joins the pieces of the item that CTA blockIdx.x began and did not finish, rows
-// [blockIdx.y * 8, +8) of the tile, a row per warp: m = max of the pieces', l and O summed with
-// each piece scaled by 2^(m_i - m). Launched with programmatic dependence: it waits on the device
-// for the attention kernel's end, so its launch costs no gap.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p, int R) {
+// Joins the pieces of the item that CTA blockIdx.x began and did not finish: m = max of the pieces', l
+// and O summed with each piece scaled by 2^(m_i - m). A warp takes 32 rows (R = 16: 16 rows, two
+// columns side by side) and 8 columns of them: a piece's column is one coalesced load, and those of four
+// pieces are in flight (32 columns a warp and one piece at a time took 29 us for 16 items of 9
+// pieces; the sum of an item's pieces is latency, not bytes). Launched with programmatic dependence: it waits on the device for the attention
+// kernel's end, so its launch costs no gap.
+template <int D, bool BF16, int R>
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p) {
+    constexpr int LR = R < 32 ? R : 32, CL = 32 / LR;  // rows of a warp, columns of one load
+    constexpr int COLS = 8, LOADS = COLS / CL;
+    constexpr int UNITS = (R / LR) * (D / COLS);       // warps' work of a whole tile
     pdl_wait();
-    const int4 d = p.desc[blockIdx.x];  // sequence, key head, row tile, pieces
-    if (d.w < 2) return;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const ChunkSeq s = chunk_seq(p, d.x);
-    const int row = d.z * R + r;
-    if (r >= R || row >= s.rows) return;
-    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * R + r; };
+    const ChunkDesc d = p.desc[blockIdx.x];
+    if (d.pieces < 2) return;
+    const int lane = threadIdx.x & 31, rl = lane % LR, cl = lane / LR;
+    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);
+    if (unit >= UNITS) return;
+    const int half = R / p.mma_tiles;                  // rows of an MMA tile
+    const int c0 = (unit % (D / COLS)) * COLS, r = (unit / (D / COLS)) * LR + rl;
+    // row r of the tile: token and head (rows past the last token of an MMA tile are nobody's)
+    const int T = p.tile_tokens / p.mma_tiles, sub = r / half, rr = r - sub * half;
+    const int ti = rr / p.G, i = sub * T + ti;
+    const bool there = ti < T && i < d.tokens;
+    if (!__any_sync(0xffffffffu, there)) return;
+    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)); };
     float m = -INFINITY;
-    for (int i = lane; i < d.w; i += 32) m = fmaxf(m, p.part_ml[slot(i)].x);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    constexpr int CPL = D / 32;  // columns a lane
-    float acc[CPL], l = 0.f;
-#pragma unroll
-    for (int k = 0; k < CPL; ++k) acc[k] = 0.f;
-    if (m != -INFINITY) {
 #pragma unroll 4
-        for (int i = 0; i < d.w; ++i) {
-            const float2 ml = p.part_ml[slot(i)];
-            const float a = ex2_approx(ml.x - m);  // a piece that saw nothing: 2^-inf = 0
-            l = fmaf(ml.y, a, l);
-            const float *o = p.part_o + slot(i) * D;
-            if constexpr (CPL == 1) {
-                acc[0] = fmaf(o[lane], a, acc[0]);
-            } else {
+    for (int k = 0; k < d.pieces; ++k) m = fmaxf(m, p.part_ml[slot(k) * R + r].x);
+    if (!there) m = -INFINITY;
+    float acc[LOADS], l = 0.f;
 #pragma unroll
-                for (int k = 0; k < CPL / 2; ++k) {
-                    const float2 v = *reinterpret_cast<const float2 *>(o + k * 64 + 2 * lane);
-                    acc[2 * k] = fmaf(v.x, a, acc[2 * k]);
-                    acc[2 * k + 1] = fmaf(v.y, a, acc[2 * k + 1]);
-                }
-            }
-        }
+    for (int c = 0; c < LOADS; ++c) acc[c] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < d.pieces; ++k) {
+        const float2 ml = p.part_ml[slot(k) * R + r];
+        // a piece in which the row saw nothing adds nothing
+        const float a = m == -INFINITY || ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        const float *o = p.part_o + (slot(k) * D + c0 + cl) * R + r;
+        float v[LOADS];
+#pragma unroll
+        for (int c = 0; c < LOADS; ++c) v[c] = o[static_cast<int64_t>(c) * CL * R];
+        l = a > 0.f ? fmaf(ml.y, a, l) : l;
+#pragma unroll
+        for (int c = 0; c < LOADS; ++c) acc[c] = fmaf(v[c], a, acc[c]);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t tok = s.q0 + row / p.G;
-    const int head = d.y * p.G + row % p.G;
-    uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D;
-    if constexpr (CPL == 1) {
-        const uint32_t u = BF16 ? pack2_bf16(acc[0] * inv, 0.f) : pack2_f16(acc[0] * inv, 0.f);
-        out[lane] = static_cast<uint16_t>(u);
-    } else {
+    const int64_t tok = d.token + i;
+    const int head = d.head + rr - ti * p.G;
+    uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D + c0;
+    if constexpr (CL == 1) {
+        if (there) {
 #pragma unroll
-        for (int k = 0; k < CPL / 2; ++k) {
-            const float x = acc[2 * k] * inv, y = acc[2 * k + 1] * inv;
-            *reinterpret_cast<uint32_t *>(out + k * 64 + 2 * lane) = BF16 ? pack2_bf16(x, y) : pack2_f16(x, y);
+            for (int c = 0; c < COLS; c += 8) {
+                uint32_t x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float lo = acc[c + 2 * q] * inv, hi = acc[c + 2 * q + 1] * inv;
+                    x[q] = BF16 ? pack2_bf16(lo, hi) : pack2_f16(lo, hi);
+                }
+                *reinterpret_cast<uint4 *>(out + c) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        }
+    } else {  // this lane holds columns cl, cl + 2, ... of its row
+        static_assert(CL == 1 || CL == 2, "rows of a tile");
+#pragma unroll
+        for (int c = 0; c < LOADS; ++c) {
+            const float other = __shfl_xor_sync(0xffffffffu, acc[c], LR);
+            if (there && cl == 0)
+                *reinterpret_cast<uint32_t *>(out + c * 2) = BF16 ? pack2_bf16(acc[c] * inv, other * inv)
+                                                                  : pack2_f16(acc[c] * inv, other * inv);
         }
     }
-    if (p.lse && lane == 0)
+    if (p.lse && there && c0 == 0 && cl == 0)
         p.lse[static_cast<int64_t>(head) * p.total + tok] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
 }
 
-template <int D, bool BF16>
-static cudaError_t launch_combine(const ChunkParams &p, int R, int ctas, cudaStream_t st) {
+template <int D, bool BF16, int R>
+static cudaError_t launch_combine(const ChunkParams &p, int ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, (R + 7) / 8, 1);
+    cfg.gridDim = dim3(ctas, ((R < 32 ? 1 : R / 32) * (D / 8) + 7) / 8, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -294,7 +328,7 @@ static cudaError_t launch_combine(const ChunkParams &p, int R, int ctas, cudaStr
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_combine_kernel<D, BF16>, p, R);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, chunk_combine_kernel<D, BF16, R>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

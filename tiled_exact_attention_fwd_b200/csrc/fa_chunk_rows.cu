@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 1)
 chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
     using C = RowsCfg<D>;
     constexpr int R = C::R, BN = C::BN, KPW = C::KPW, SW = C::SW, NS = C::NS;
-    using Walk = ChunkWalk<R, BN, CAUSAL>;
+    using Walk = ChunkWalk<1, BN, CAUSAL>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *sO = reinterpret_cast<float *>(smem + C::OFF_O);
@@ -83,7 +83,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    if (warp == 0) chunk_locate<R, BN, CAUSAL>(p, blockIdx.x, gridDim.x, start);
+    if (warp == 0) chunk_locate<1, BN, CAUSAL>(p, blockIdx.x, gridDim.x, start);
     __syncthreads();
     const ChunkStart st = *start;
 
@@ -133,7 +133,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         constexpr int CPB = SW / 16;
         bool ok = true;
         int u = 0;
-        int4 desc = make_int4(0, 0, 0, 0);
+        ChunkDesc desc{0, 0, 0, 0};
         Walk w;
         for (bool more = w.begin(p, st); more; more = w.next(p)) {
             // Q rows g and g + 8 of the tile as A fragments
@@ -141,19 +141,16 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const uint32_t *q0 = nullptr, *q1 = nullptr;
             int lim0 = w.keys, lim1 = w.keys;  // keys each row sees (rows past the last: any)
             {
-                const int r0 = w.t * R + g, r1 = r0 + 8;
-                if (r0 < w.s.rows) {
-                    const int i = r0 / p.G;
-                    lim0 = token_keys<CAUSAL>(w.s, i);
-                    q0 = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q) +
-                                                            (static_cast<int64_t>(w.s.q0 + i) * p.Hq + w.h * p.G + r0 % p.G) * D);
-                }
-                if (r1 < w.s.rows) {
-                    const int i = r1 / p.G;
-                    lim1 = token_keys<CAUSAL>(w.s, i);
-                    q1 = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q) +
-                                                            (static_cast<int64_t>(w.s.q0 + i) * p.Hq + w.h * p.G + r1 % p.G) * D);
-                }
+                const int rows = w.tokens * p.G;
+                auto row = [&](int r, int &lim) -> const uint32_t * {
+                    if (r >= rows) return nullptr;
+                    const int i = w.i0 + r / p.G;
+                    lim = token_keys<CAUSAL>(w.s, i);
+                    return reinterpret_cast<const uint32_t *>(
+                        static_cast<const uint16_t *>(p.q) + (static_cast<int64_t>(w.s.q0 + i) * p.Hq + w.h * p.G + r % p.G) * D);
+                };
+                q0 = row(g, lim0);
+                q1 = row(g + 8, lim1);
             }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -162,7 +159,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 qf[k][2] = q0 ? __ldg(q0 + k * 8 + 4 + t4) : 0u;
                 qf[k][3] = q1 ? __ldg(q1 + k * 8 + 4 + t4) : 0u;
             }
-            const int all_see = CAUSAL ? token_keys<CAUSAL>(w.s, (w.t * R) / p.G) : w.keys;  // keys that every row sees
+            const int all_see = CAUSAL ? token_keys<CAUSAL>(w.s, w.i0) : w.keys;  // keys that every row sees
             float o[D / 8][4];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
@@ -274,6 +271,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 sML[warp * R + g + 8] = make_float2(m1, l1);
             }
             const bool whole = w.whole();
+            const int rows = w.tokens * p.G;
             const int row = threadIdx.x >> 3, col8 = threadIdx.x & 7;  // 8 threads a row
 #pragma unroll
             for (int half = 0; half < D / C::DH; ++half) {
@@ -281,13 +279,13 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const float *oi = o[half * NT + i];
-                    if (g < w.rows)
+                    if (g < rows)
                         *reinterpret_cast<float2 *>(sO + (warp * R + g) * C::OROW + i * 8 + 2 * t4) = make_float2(oi[0], oi[1]);
-                    if (g + 8 < w.rows)
+                    if (g + 8 < rows)
                         *reinterpret_cast<float2 *>(sO + (warp * R + g + 8) * C::OROW + i * 8 + 2 * t4) = make_float2(oi[2], oi[3]);
                 }
                 consumers_sync();
-                if (row < w.rows) {
+                if (row < rows) {
                     float m = -INFINITY, l = 0.f, a[C::NW];
 #pragma unroll
                     for (int v = 0; v < C::NW; ++v) m = fmaxf(m, sML[v * R + row].x);
@@ -297,13 +295,12 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         a[v] = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
                         l = fmaf(ml.y, a[v], l);
                     }
-                    const int pr = w.t * R + row;
-                    const int64_t tok = w.s.q0 + pr / p.G;
-                    const int head = w.h * p.G + pr % p.G;
+                    const int64_t tok = w.s.q0 + w.i0 + row / p.G;
+                    const int head = w.h * p.G + row % p.G;
                     const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
                     uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D + half * C::DH;
-                    const int64_t slot = static_cast<int64_t>(w.slot()) * R + row;
-                    float *po = p.part_o + slot * D + half * C::DH;
+                    const int64_t slot = w.slot();
+                    float *po = p.part_o + (slot * D + half * C::DH) * R + row;
 #pragma unroll
                     for (int c = 0; c < C::DH / 32; ++c) {
                         const int col = c * 32 + col8 * 4;
@@ -316,15 +313,19 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             x.z = fmaf(y.z, a[v], x.z);
                             x.w = fmaf(y.w, a[v], x.w);
                         }
-                        if (whole)
+                        if (whole) {
                             *reinterpret_cast<uint2 *>(out + col) =
                                 make_uint2(pack16<BF16>(x.x * inv, x.y * inv), pack16<BF16>(x.z * inv, x.w * inv));
-                        else
-                            *reinterpret_cast<float4 *>(po + col) = x;
+                        } else {
+                            po[col * R] = x.x;
+                            po[(col + 1) * R] = x.y;
+                            po[(col + 2) * R] = x.z;
+                            po[(col + 3) * R] = x.w;
+                        }
                     }
                     if (half == 0 && col8 == 0) {
                         if (!whole)
-                            p.part_ml[slot] = make_float2(m, l);
+                            p.part_ml[slot * R + row] = make_float2(m, l);
                         else if (p.lse)
                             p.lse[static_cast<int64_t>(head) * p.total + tok] =
                                 l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
@@ -332,7 +333,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
                 consumers_sync();
             }
-            if (w.j0 == 0 && w.j1 < w.steps) desc = make_int4(w.b, w.h, w.t, w.pieces(st.per));
+            if (w.j0 == 0 && w.j1 < w.steps) desc = w.desc(p, st.per);
         }
         if (threadIdx.x == 0) p.desc[blockIdx.x] = desc;
     }
@@ -355,7 +356,7 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const ChunkPara
     }
     kern<<<ctas, C::THREADS, C::SMEM, st>>>(tk, tv, p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_combine<D, BF16>(p, C::R, ctas, st);
+    return e != cudaSuccess ? e : launch_combine<D, BF16, C::R>(p, ctas, st);
 }
 
 template <int D>

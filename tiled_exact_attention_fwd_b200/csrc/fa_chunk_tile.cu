@@ -2,7 +2,8 @@
 // (fa_fwd_paged_chunk; prompt chunks): tiles of 128 rows on the tensor core.
 //
 // Rows are (new token, query head of the group), so a tile of a call with shared key heads holds
-// 128 / G tokens and every K/V tile that is loaded serves all of them. A CTA walks its run of steps
+// 128 / G tokens (whole ones: G = 6 fills 126 rows) and every K/V tile that is loaded serves all of
+// them. A CTA walks its run of steps
 // (fa_chunk.cuh), each one 128-key tile against two 128-row tiles A and B (one at D = 256, where two
 // O accumulators do not fit in TMEM), with the roles of the dense forward:
 //   warps 0-3, 4-7  softmax of tile A, B: a thread per row; running maximum and sum in registers, P
@@ -13,10 +14,9 @@
 //                   works on one while the softmax of the other runs. Before an item's last PV it clears
 //                   the rows of V past the last key.
 //   warp 10         D <= 64: issues the PVs (warp 9 then the QKs only).
-//   warp 11         gathers the Q rows (any group size) with cp.async into the swizzled tiles once the
-//                   last item's QKs have read them.
-// Rows of a tile past the sequence's last are zeros in Q and are not stored; a softmax warp without
-// a row skips the exponentials. An item that the split cuts leaves O, m and l in the workspace.
+//   warp 11         Q tiles by TMA, each once the last item's QKs have read its buffer.
+// Rows of a tile past the sequence's last are computed on whatever lies there and not stored; a
+// softmax warp without a row skips the exponentials. An item that the split cuts leaves O, m and l in the workspace.
 #include "fa_chunk.cuh"
 #include "fa_fwd_kernel.cuh"
 
@@ -39,9 +39,10 @@ struct TileCfg : Cfg<D> {
 
 template <int D, bool BF16, bool CAUSAL>
 __global__ void __launch_bounds__(TileCfg<D>::NUM_THREADS, 1)
-chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
+chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
     using C = TileCfg<D>;
-    using Walk = ChunkWalk<C::R, C::BN, CAUSAL>;
+    using Walk = ChunkWalk<C::MAXQ, C::BN, CAUSAL>;
     constexpr int BM = C::BM, BN = C::BN, SW = C::SW, NS = C::NS, U = C::UNITS;
     constexpr bool SINGLE = C::MAXQ == 1, DEC = C::DECOUPLED;
     constexpr int CPB = SW / 16;
@@ -61,7 +62,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     pdl_launch_dependents();
     if (threadIdx.x == 32 * W_TMA) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&q_full[t], 32);
+            mbar_init(&q_full[t], 1);
             mbar_init(&q_free[t], 1);
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 128);
@@ -75,6 +76,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         mbar_init(drain, DEC ? 2 : 1);
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
@@ -82,11 +84,12 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
-    if (warp == 0) chunk_locate<C::R, BN, CAUSAL>(p, blockIdx.x, gridDim.x, start);
+    if (warp == 0) chunk_locate<C::MAXQ, BN, CAUSAL>(p, blockIdx.x, gridDim.x, start);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    const int TT = p.tile_tokens / C::MAXQ;  // tokens of an MMA tile
 
     if (warp >= C::NUM_SOFTMAX_WARPS) {
         if constexpr (C::SPLIT_REGS) regs_dec<C::regs_low(false)>();
@@ -145,10 +148,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             // S_t = Q_t K_jj^T; `first`: the first tile to use this K, `last`: the last
             auto qk = [&](int t, int jj, bool first, bool last, bool item_end) {
                 const int gs = (t ? gb : ga) + jj, buf = SINGLE ? (gs & 1) : t;
-                if (jj == 0) {
-                    if (!wait(&q_full[t], nq[t] & 1, 760 + t)) return;
-                    fence_proxy_async_smem();  // Q was written by cp.async
-                }
+                if (jj == 0 && !wait(&q_full[t], nq[t] & 1, 760 + t)) return;
                 if (DEC && gs > 0 && !wait(&s_free[t], (gs - 1) & 1, 762 + t)) return;
                 tc_fence_after_sync();
                 constexpr uint32_t idesc = idesc_f16(BM, BN, BF16, false), dhi = smem_desc_hi(8 * SW, C::LAYOUT);
@@ -219,7 +219,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const bool do_qk = !DEC || warp == W_MMA, do_pv = !DEC || warp == W_PV;
             for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
                 const int n = w.j1 - w.j0;
-                const bool two = !SINGLE && w.rows > BM;
+                const bool two = !SINGLE && w.tokens > TT;
                 const int end = w.keys - w.j0 * BN;  // keys of the segment (its last tile may reach past them)
                 auto valid = [&](int jj) { return max(0, end - jj * BN); };
                 if (SINGLE) {
@@ -261,40 +261,36 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             while (!mbar_try_wait(drain, 0) && global_timer_ns() - t0 < lim) {
             }
         } else if (warp == W_Q) {
-            // ------------------------------------------------------------ Q rows
-            bool ok = true;
-            int nq[2] = {0, 0};
-            auto wait = [&](uint64_t *bar, uint32_t ph, int where) {
-                if (ok) ok = __all_sync(0xffffffffu, wait_bounded(bar, ph, abort_flag, lim, where));
-                return ok;
-            };
-            for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
-                const bool two = !SINGLE && w.rows > BM;
-                for (int t = 0; t < (two ? 2 : 1); ++t) {
-                    if (nq[t] > 0 && !wait(&q_free[t], (nq[t] - 1) & 1, 770 + t)) break;
-                    const uint32_t dst = smem_u32(sQ + t * C::Q_BYTES);
-                    for (int g = 0; g < BM; g += 32) {
-                        // this lane's row of the group: its place in q, or nowhere (zeros)
-                        const int pr = w.t * C::R + t * BM + g + lane;
-                        const bool there = pr < w.s.rows;
-                        const int i = there ? pr / p.G : 0;
-                        const int64_t at = (static_cast<int64_t>(w.s.q0 + i) * p.Hq + w.h * p.G + (there ? pr - i * p.G : 0)) * D;
-                        constexpr int CPR = D / 8;
-#pragma unroll 4
-                        for (int k = 0; k < CPR; ++k) {
-                            const int idx = k * 32 + lane, rr = idx / CPR, ch = idx % CPR, r = g + rr;
-                            const int64_t src = __shfl_sync(0xffffffffu, at, rr);
-                            const bool ok_row = __shfl_sync(0xffffffffu, there, rr);
-                            const int swz = SW == 128 ? (r & 7) : ((r >> 1) & 3);
-                            cp_async_16_zfill(dst + (ch / CPB) * BM * SW + r * SW + (((ch % CPB) ^ swz) << 4),
-                                              static_cast<const uint16_t *>(p.q) + src + ch * 8, ok_row ? 16u : 0u);
+            // ------------------------------------------------------------ Q tiles
+            // One box per column block: the G heads of TT tokens, rows token-major. Rows past them are
+            // never written: they hold whatever was there, and nobody reads their results.
+            if (lane == 0) {
+                bool ok = true;
+                int nq[2] = {0, 0};
+                const uint64_t pol = l2_policy_evict_first();
+                for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
+                    const bool two = !SINGLE && w.tokens > TT;
+                    for (int t = 0; t < (two ? 2 : 1); ++t) {
+                        if (nq[t] > 0 && !wait_bounded(&q_free[t], (nq[t] - 1) & 1, abort_flag, lim, 770 + t)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&q_full[t], TT * p.G * D * 2);
+#pragma unroll
+                        for (int blk = 0; blk < C::NBLK; ++blk)
+                            tma_load_4d(sQ + t * C::Q_BYTES + blk * BM * SW, &tm_q, &q_full[t], blk * C::SWE, 0, w.h,
+                                        w.s.q0 + w.i0 + t * TT, pol);
+                        nq[t]++;
+                    }
+                }
+                if (*abort_flag) {  // the copies in flight land before the shared memory goes away
+                    for (int t = 0; t < 2; ++t) {
+                        const uint64_t t0 = global_timer_ns();
+                        while (nq[t] > 0 && !mbar_try_wait(&q_full[t], (nq[t] - 1) & 1) && global_timer_ns() - t0 < lim) {
                         }
                     }
-                    cp_async_mbar_arrive(&q_full[t]);
-                    nq[t]++;
                 }
             }
-            cp_async_wait_all();
         }
     } else {
         // ------------------------------------------------------------ softmax + epilogue
@@ -305,18 +301,18 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const float sc = p.scale_log2;
         bool ok = true;
         int gbase = 0;
-        int4 desc = make_int4(0, 0, 0, 0);
+        ChunkDesc desc{0, 0, 0, 0};
         Walk w;
 #pragma unroll 1
         for (bool more = w.begin(p, *start); more; more = w.next(p)) {
-            if (w.j0 == 0 && w.j1 < w.steps) desc = make_int4(w.b, w.h, w.t, w.pieces(start->per));
-            if (t == 1 && w.rows <= BM) continue;  // tile absent
+            if (w.j0 == 0 && w.j1 < w.steps) desc = w.desc(p, start->per);
+            if (t == 1 && w.tokens <= TT) continue;  // tile absent
             const int n = w.j1 - w.j0;
-            const int pr = w.t * C::R + t * BM + r;
-            const bool row_ok = pr < w.s.rows;
-            const bool busy = w.t * C::R + t * BM + quarter * 32 < w.s.rows;  // this warp has a row
+            const int rows = min(w.tokens - t * TT, TT) * p.G;  // of this MMA tile
+            const bool row_ok = r < rows;
+            const bool busy = quarter * 32 < rows;  // this warp has a row
             // keys this row sees, counted from the segment's first
-            int hi = (row_ok ? token_keys<CAUSAL>(w.s, pr / p.G) : w.keys) - w.j0 * BN;
+            int hi = (row_ok ? token_keys<CAUSAL>(w.s, w.i0 + t * TT + r / p.G) : w.keys) - w.j0 * BN;
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
             for (int jj = 0; ok && jj < n; ++jj, hi -= BN) {
@@ -420,43 +416,42 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             if (!ok || !busy) continue;
             tc_fence_after_sync();
             const bool whole = w.whole();
-            const int i = pr / p.G;
-            const int64_t tok = w.s.q0 + i;
-            const int head = w.h * p.G + pr - i * p.G;
-            const int64_t slot = static_cast<int64_t>(w.slot()) * C::R + t * BM + r;
+            const int ti = r / p.G;
+            const int64_t tok = w.s.q0 + w.i0 + t * TT + ti;
+            const int head = w.h * p.G + r - ti * p.G;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D;
-            float *po = p.part_o + slot * D;
+            const int64_t slot = w.slot();
+            float *po = p.part_o + slot * D * C::R + t * BM + r;  // column by column
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_addr + c0, o);
                 tmem_ld_wait();
                 tmem_reg_fence<32>(o);
-                if (row_ok) {
-                    if (whole) {
+                if (!whole) {
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint32_t x[4];
+                    for (int v = 0; v < 32; ++v) po[(c0 + v) * C::R] = __uint_as_float(o[v]);
+                } else if (row_ok) {
+                    uint32_t x[16];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                x[k] = pack2<BF16>(__uint_as_float(o[v * 8 + 2 * k]) * inv, __uint_as_float(o[v * 8 + 2 * k + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(out + c0 + v * 8) = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
+                    for (int k = 0; k < 16; ++k)
+                        x[k] = pack2<BF16>(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+                    if (p.out_align32) {
+                        st_global_v8(out + c0, x);
+                        st_global_v8(out + c0 + 16, x + 8);
                     } else {
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            *reinterpret_cast<uint4 *>(po + c0 + v * 4) = make_uint4(o[v * 4], o[v * 4 + 1], o[v * 4 + 2], o[v * 4 + 3]);
+                        for (int v = 0; v < 4; ++v)
+                            *reinterpret_cast<uint4 *>(out + c0 + v * 8) = make_uint4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
                     }
                 }
                 __syncwarp();
             }
-            if (row_ok) {
-                if (!whole)
-                    p.part_ml[slot] = make_float2(m, l);
-                else if (p.lse)
-                    p.lse[static_cast<int64_t>(head) * p.total + tok] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
-            }
+            if (!whole)
+                p.part_ml[slot * C::R + t * BM + r] = make_float2(m, l);
+            else if (row_ok && p.lse)
+                p.lse[static_cast<int64_t>(head) * p.total + tok] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
         }
         if (threadIdx.x == 0) p.desc[blockIdx.x] = desc;
     }
@@ -469,7 +464,8 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 }
 
 template <int D, bool BF16, bool CAUSAL>
-cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p, int ctas, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p, int ctas,
+                   cudaStream_t st) {
     using C = TileCfg<D>;
     auto kern = chunk_tile_kernel<D, BF16, CAUSAL>;
     static uint64_t attr_set_mask = 0;  // per device; setting it twice is harmless
@@ -490,27 +486,27 @@ cudaError_t launch(const CUtensorMap &tk, const CUtensorMap &tv, const ChunkPara
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_set_mask, bit, __ATOMIC_RELEASE);
     }
-    kern<<<ctas, C::NUM_THREADS, C::SMEM_BYTES, st>>>(tk, tv, p);
+    kern<<<ctas, C::NUM_THREADS, C::SMEM_BYTES, st>>>(tq, tk, tv, p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_combine<D, BF16>(p, C::R, ctas, st);
+    return e != cudaSuccess ? e : launch_combine<D, BF16, C::R>(p, ctas, st);
 }
 
 template <int D>
-cudaError_t launch_d(bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv, const ChunkParams &p, int ctas,
-                     cudaStream_t st) {
-    if (bf16) return causal ? launch<D, true, true>(tk, tv, p, ctas, st) : launch<D, true, false>(tk, tv, p, ctas, st);
-    return causal ? launch<D, false, true>(tk, tv, p, ctas, st) : launch<D, false, false>(tk, tv, p, ctas, st);
+cudaError_t launch_d(bool bf16, bool causal, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                     const ChunkParams &p, int ctas, cudaStream_t st) {
+    if (bf16) return causal ? launch<D, true, true>(tq, tk, tv, p, ctas, st) : launch<D, true, false>(tq, tk, tv, p, ctas, st);
+    return causal ? launch<D, false, true>(tq, tk, tv, p, ctas, st) : launch<D, false, false>(tq, tk, tv, p, ctas, st);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_tile(int D, bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv,
-                              const ChunkParams &p, int ctas, cudaStream_t st) {
+cudaError_t launch_chunk_tile(int D, bool bf16, bool causal, const CUtensorMap &tq, const CUtensorMap &tk,
+                              const CUtensorMap &tv, const ChunkParams &p, int ctas, cudaStream_t st) {
     switch (D) {
-        case 32: return launch_d<32>(bf16, causal, tk, tv, p, ctas, st);
-        case 64: return launch_d<64>(bf16, causal, tk, tv, p, ctas, st);
-        case 128: return launch_d<128>(bf16, causal, tk, tv, p, ctas, st);
-        case 256: return launch_d<256>(bf16, causal, tk, tv, p, ctas, st);
+        case 32: return launch_d<32>(bf16, causal, tq, tk, tv, p, ctas, st);
+        case 64: return launch_d<64>(bf16, causal, tq, tk, tv, p, ctas, st);
+        case 128: return launch_d<128>(bf16, causal, tq, tk, tv, p, ctas, st);
+        case 256: return launch_d<256>(bf16, causal, tq, tk, tv, p, ctas, st);
         default: return cudaErrorInvalidValue;
     }
 }

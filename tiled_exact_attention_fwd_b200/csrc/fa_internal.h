@@ -14,6 +14,10 @@ uint64_t host_wait_limit_ns();
 int host_sm_count();
 bool host_head_dim_ok(int D);
 bool host_encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows);
+// The same tensor with its heads in Hkv groups of G: boxes of `inner` elements of one group's G heads of
+// `tokens` tokens (rows token-major, the group's heads within a token).
+bool host_encode_group_map(CUtensorMap *m, const void *base, bool bf16, int D, int G, int Hkv, int64_t N, int inner,
+                           int tokens);
 
 // Kernel parameters of the attention forward (passed by value).
 struct FwdParams {
@@ -135,6 +139,11 @@ constexpr int kQkNormBwdCtas = 592;
 cudaError_t launch_qk_norm(int D, bool bf16, bool interleaved, bool backward, const QkNormParams &p, cudaStream_t st);
 cudaError_t qk_norm_error_addrs(int **code, int **where);
 
+// An item whose pieces are joined: how many (0: none), first token row, tokens, first query head.
+struct ChunkDesc {
+    int pieces, token, tokens, head;
+};
+
 // New tokens over a paged cache (fa_chunk.cuh).
 struct ChunkParams {
     const void *q;                              // (total, Hq, D)
@@ -149,9 +158,11 @@ struct ChunkParams {
     int Hq, Hkv, G;                             // G = Hq / Hkv
     float scale_log2;
     uint64_t timeout_ns;
-    int min_steps;                              // least steps of a CTA's run
-    // workspace: per CTA (sequence, key head, row tile, pieces); per slot and row (m, l) and O
-    int4 *desc;
+    int tile_tokens, mma_tiles;                 // tokens of a row tile; MMA tiles that they lie in
+    int min_cost;                               // least cost of a CTA's run (at least a step's)
+    int out_align32;                            // out is 32-byte aligned
+    // workspace: per CTA the item it begins and leaves; per slot and row (m, l); per slot O by columns
+    ChunkDesc *desc;
     float2 *part_ml;
     float *part_o;
 };
@@ -163,8 +174,9 @@ int chunk_rows_tile();
 int chunk_rows_box(int D, int page_size);       // rows of a K or V box
 cudaError_t chunk_rows_error_addrs(int **code, int **where);
 // Tiles of 128 rows on the tensor core, two at a time at D <= 128 (fa_chunk_tile.cu).
-cudaError_t launch_chunk_tile(int D, bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv,
-                              const ChunkParams &p, int ctas, cudaStream_t st);
+// tq: map of q as (total, Hkv, G, D) with boxes of a tile's tokens.
+cudaError_t launch_chunk_tile(int D, bool bf16, bool causal, const CUtensorMap &tq, const CUtensorMap &tk,
+                              const CUtensorMap &tv, const ChunkParams &p, int ctas, cudaStream_t st);
 int chunk_tile_rows(int D);
 int chunk_tile_k_box(int D, int page_size);
 int chunk_tile_v_box(int D, int page_size);

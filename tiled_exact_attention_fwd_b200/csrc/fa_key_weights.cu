@@ -41,8 +41,8 @@ struct KeyWalk {
     int b, h, j, jn, t0, tiles;
     int64_t left;  // row tiles of the run that are left
     __device__ static int64_t head_cost(const ChunkParams &p, const ChunkSeq &s) {
-        if (s.rows == 0) return 0;
-        const int tiles = (s.rows + R - 1) / R, jn = (s.kv + BN - 1) / BN;
+        if (s.n == 0) return 0;
+        const int tiles = (s.n * p.G + R - 1) / R, jn = (s.kv + BN - 1) / BN;
         if (!CAUSAL) return static_cast<int64_t>(tiles) * jn;
         int64_t sum = 0;
         for (int j = 0; j < jn; ++j) sum += tiles - first_tile<R, BN, CAUSAL>(p, s, j);
@@ -51,7 +51,7 @@ struct KeyWalk {
     __device__ __forceinline__ void seq(const ChunkParams &p) {
         s = chunk_seq(p, b);
         jn = (s.kv + BN - 1) / BN;
-        tiles = (s.rows + R - 1) / R;
+        tiles = (s.n * p.G + R - 1) / R;
     }
     // one warp: where run `cta` begins (st->j: key tile); a run takes the items that begin in it
     __device__ static void locate(const ChunkParams &p, int cta, int ctas, KeyStart *st) {
@@ -93,7 +93,7 @@ struct KeyWalk {
                     if (start >= at && start < at + cost[i]) {
                         const int b = base + lane * PER + i;
                         const ChunkSeq s = chunk_seq(p, b);
-                        const int tiles = (s.rows + R - 1) / R;
+                        const int tiles = (s.n * p.G + R - 1) / R;
                         int64_t rem = start - at;
                         const int64_t one = cost[i] / p.Hkv;
                         int h = static_cast<int>(rem / one);
@@ -126,9 +126,9 @@ struct KeyWalk {
     }
     // j may be one past the head's last tile: on to the next head or sequence
     __device__ __forceinline__ bool settle(const ChunkParams &p) {
-        while (j >= jn || s.rows == 0) {
+        while (j >= jn || s.n == 0) {
             j = 0;
-            if (s.rows == 0 || jn == 0 || ++h == p.Hkv) {
+            if (s.n == 0 || jn == 0 || ++h == p.Hkv) {
                 h = 0;
                 if (++b >= p.num_seqs) return false;
                 seq(p);
@@ -247,7 +247,7 @@ key_weights_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const ChunkPar
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int pr = t * R + i * 8 + g;
-                        const bool there = pr < w.s.rows;
+                        const bool there = pr < w.s.n * p.G;
                         const int64_t tok = w.s.q0 + (there ? pr / p.G : 0);
                         const uint32_t *q = reinterpret_cast<const uint32_t *>(
                             static_cast<const uint16_t *>(p.q) + (tok * p.Hq + w.h * p.G + (there ? pr % p.G : 0)) * D);
@@ -261,7 +261,7 @@ key_weights_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const ChunkPar
                             const int r = t * R + i * 8 + 2 * t4 + k;
                             lim[i][k] = 0;
                             ls[i][k] = 0.f;
-                            if (r < w.s.rows) {
+                            if (r < w.s.n * p.G) {
                                 const float x = p.lse_in[static_cast<int64_t>(w.h * p.G + r % p.G) * p.total + w.s.q0 + r / p.G];
                                 ls[i][k] = x * 1.4426950408889634f;
                                 // a row that saw nothing gives no weight
