@@ -345,14 +345,17 @@ FA_API fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const vo
  *                rows give nothing).
  *   weights      float32 (num_seqs, Hkv, width), width >= max_blocks_per_seq * page_size; slots at and
  *                past kv_lens[b] are not touched. Each sum is formed in a fixed order.
- * Calls that overlap on the GPU must not share `weights`.
+ *   workspace    fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len) bytes, 256-byte aligned, contents of
+ *                no matter (0 bytes where a key head has at most 16 rows: NULL will do).
+ * Calls that overlap on the GPU must share neither `weights` nor the workspace.
  */
+FA_API int64_t fa_paged_key_weights_workspace(int Hq, int Hkv, int D, int max_q_len);
 FA_API fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t *block_table,
                                       int max_blocks_per_seq, int page_size, int num_pages,
                                       const int32_t *cu_seqlens, const int32_t *kv_lens, int num_seqs,
                                       int total, int max_q_len, const float *lse, float *weights,
-                                      int64_t width, int Hq, int Hkv, int D, float scale, int causal,
-                                      fa_dtype dtype, void *stream);
+                                      int64_t width, void *workspace, int64_t workspace_bytes, int Hq,
+                                      int Hkv, int D, float scale, int causal, fa_dtype dtype, void *stream);
 
 /*
  * Eviction from a paged cache: every sequence and key head of more than `budget` keys keeps its last

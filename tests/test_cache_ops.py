@@ -165,18 +165,19 @@ class TestRefusals:
 
     def test_chunk_workspace(self, lib):
         assert lib.fa_fwd_paged_chunk_workspace(4, 2, 64, 1) > 0
-        for bad in [(5, 2, 64, 1), (4, 0, 64, 1), (4, 2, 65, 1), (4, 2, 64, -1)]:
-            assert lib.fa_fwd_paged_chunk_workspace(*bad) == 0
+        for bad in [(5, 2, 64, 1), (129, 1, 64, 1), (4, 0, 64, 1), (4, 2, 65, 1), (4, 2, 64, -1)]:
+            assert lib.fa_fwd_paged_chunk_workspace(*bad) == 0 and lib.fa_paged_key_weights_workspace(*bad) == 0
 
     def keys(self, lib, **kw):
         a = dict(q=self.P, kc=self.P, bt=self.P, mb=4, page=16, pages=9, cu=self.P, kv=self.P, num=2, total=4, mq=2,
-                 lse=self.P, w=self.P, width=64, hq=4, hk=2, d=64, scale=0.0, causal=1, dt=0)
+                 lse=self.P, w=self.P, width=64, ws=self.P, wsb=1 << 30, hq=4, hk=2, d=64, scale=0.0, causal=1, dt=0)
         a.update(kw)
         return lib.fa_paged_key_weights(*a.values(), None)
 
     @pytest.mark.parametrize("change,status", [
         (dict(dt=5), -3), (dict(d=80), -4), (dict(hq=3), -2), (dict(width=63), -2), (dict(lse=None), -1), (dict(w=None), -1),
-        (dict(w=4097), -5), (dict(kc=4100), -5), (dict(total=0), 0)])
+        (dict(w=4097), -5), (dict(kc=4100), -5), (dict(mq=9, ws=None), -1), (dict(mq=9, wsb=1000), -2),
+        (dict(mq=9, ws=4096 + 16), -5), (dict(total=0), 0)])
     def test_key_weights(self, lib, change, status):
         assert self.keys(lib, **change) == status
 

@@ -71,15 +71,17 @@ def lib() -> ctypes.CDLL:
                                             i32, i32, i32, vp, vp, i32, i64, i32, i32, i32, f32, i32, i32, vp]
         L.fa_fwd_paged_chunk.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp, i64, i32, i32,
                                          i32, f32, i32, i32, vp]
-        L.fa_paged_key_weights.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, i64, i32, i32, i32,
-                                           f32, i32, i32, vp]
+        L.fa_paged_key_weights.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, i64, vp, i64, i32,
+                                           i32, i32, f32, i32, i32, vp]
         L.fa_paged_evict.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp, i64, i32, i32, vp, vp, vp, i32, i32, i32, i32, vp]
         for f in (L.fa_qk_norm_rope, L.fa_qk_norm_rope_bwd, L.fa_qk_norm_rope_paged, L.fa_fwd_paged_chunk,
                   L.fa_paged_key_weights, L.fa_paged_evict):
             f.restype = ctypes.c_int
         L.fa_qk_norm_rope_bwd_workspace.argtypes = [i32]
         L.fa_fwd_paged_chunk_workspace.argtypes = [i32, i32, i32, i32]
-        L.fa_qk_norm_rope_bwd_workspace.restype = L.fa_fwd_paged_chunk_workspace.restype = i64
+        L.fa_paged_key_weights_workspace.argtypes = [i32, i32, i32, i32]
+        for f in (L.fa_qk_norm_rope_bwd_workspace, L.fa_fwd_paged_chunk_workspace, L.fa_paged_key_weights_workspace):
+            f.restype = i64
         L.fa_device_status.argtypes = [ctypes.POINTER(ctypes.c_int), vp]
         L.fa_selftest_bounded_wait.argtypes = [ctypes.c_uint64, vp]
         for f in (L.fa_fwd, L.fa_fwd_paged, L.fa_bwd, L.fa_bwd_noalloc, L.fa_varlen_bwd, L.fa_varlen_fwd, L.fa_varlen_fwd_padded, L.fa_unpad, L.fa_unpad_qkv, L.fa_pad,
@@ -700,6 +702,11 @@ def fa_fwd_paged_chunk_workspace(Hq: int, Hkv: int, D: int, max_q_len: int) -> i
     return lib().fa_fwd_paged_chunk_workspace(int(Hq), int(Hkv), int(D), int(max_q_len))
 
 
+def fa_paged_key_weights_workspace(Hq: int, Hkv: int, D: int, max_q_len: int) -> int:
+    """Bytes of fa_paged_key_weights's workspace (0: none)."""
+    return lib().fa_paged_key_weights_workspace(int(Hq), int(Hkv), int(D), int(max_q_len))
+
+
 def _key_weights_args(weights, num, Hkv, dev):
     _plain("weights", weights, torch.float32, dev)
     if weights.dim() != 3 or weights.shape[0] != num or weights.shape[1] != Hkv:
@@ -708,12 +715,15 @@ def _key_weights_args(weights, num, Hkv, dev):
 
 def fa_paged_key_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
                          kv_lens: torch.Tensor, max_q_len: int, lse: torch.Tensor, weights: torch.Tensor,
-                         scale: Optional[float] = None, causal: bool = True, stream=None) -> torch.Tensor:
+                         scale: Optional[float] = None, causal: bool = True, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
     """Adds to weights (B, Hkv, width) float32 the attention weight that each cached key received from
-    the new tokens q, lse being what fa_fwd_paged_chunk returned for them. Returns weights."""
+    the new tokens q, lse being what fa_fwd_paged_chunk returned for them. Returns weights. `workspace`
+    (uint8, of fa_paged_key_weights_workspace(...) bytes) is allocated by the call unless given."""
     if _elsewhere(q, stream):
         with _on_stream(q, stream):
-            return fa_paged_key_weights(q, k_cache, block_table, cu_seqlens, kv_lens, max_q_len, lse, weights, scale, causal)
+            return fa_paged_key_weights(q, k_cache, block_table, cu_seqlens, kv_lens, max_q_len, lse, weights, scale, causal,
+                                        workspace)
     dev, num, table = _paged_args(k_cache, None, block_table, kv_lens)
     _packed_args(q, k_cache, cu_seqlens, num, dev)
     if not q.is_contiguous():
@@ -724,9 +734,18 @@ def fa_paged_key_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: to
     if lse.dim() != 2 or lse.shape[0] != Hq or lse.shape[1] != total:
         raise ValueError("lse must be (Hq, total)")
     _key_weights_args(weights, num, Hkv, dev)
-    st = lib().fa_paged_key_weights(q.data_ptr(), k_cache.data_ptr(), *table, cu_seqlens.data_ptr(), kv_lens.data_ptr(), num,
-                                    total, max_q_len, lse.data_ptr(), weights.data_ptr(), weights.shape[2], Hq, Hkv, D,
-                                    scale if scale else 0.0, causal, _dtype_code(q), _current_raw_stream(dev))
+    L = lib()
+    if workspace is None:
+        size = L.fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    else:
+        _cuda_contig("workspace", workspace)
+        _same_device(q, workspace)
+        size = workspace.numel() * workspace.element_size()
+    st = L.fa_paged_key_weights(q.data_ptr(), k_cache.data_ptr(), *table, cu_seqlens.data_ptr(), kv_lens.data_ptr(), num, total,
+                                max_q_len, lse.data_ptr(), weights.data_ptr(), weights.shape[2], _ptr(workspace), size, Hq, Hkv,
+                                D, scale if scale else 0.0, causal, _dtype_code(q), _current_raw_stream(dev))
     if st:
         raise FAError(st, "fa_paged_key_weights")
     return weights

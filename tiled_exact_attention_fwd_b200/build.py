@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
 SOURCES = ["fa_fwd.cu", "fa_fwd_paged.cu", "fa_bwd.cu", "fa_bwd256.cu", "fa_bwd_noalloc.cu", "fa_padding.cu",
-           "fa_qk_norm.cu", "fa_chunk_rows.cu", "fa_chunk_tile.cu", "fa_key_weights.cu", "fa_evict.cu", "fa_api.cu", "fa_cache_api.cu"]
+           "fa_qk_norm.cu", "fa_chunk_rows.cu", "fa_chunk_tile.cu", "fa_key_weights.cu", "fa_key_weights_tile.cu",
+           "fa_evict.cu", "fa_api.cu", "fa_cache_api.cu"]
 HEADERS = ["fa_fwd_kernel.cuh", "fa_sync.cuh", "fa_seq.cuh", "fa_ptx.cuh", "fa_chunk.cuh", "fa_mma.cuh",
            "fa_internal.h"]
 

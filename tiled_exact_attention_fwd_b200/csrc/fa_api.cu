@@ -301,7 +301,7 @@ bool bwd_aligned(const void *q, const void *k, const void *v, const void *out, c
 
 // The error words of the kernel families (one per compilation unit), read and cleared in one
 // launch on the caller's stream; the first nonzero code wins.
-constexpr int kErrorWords = 10;
+constexpr int kErrorWords = 11;
 struct ErrorWords {
     int *code[kErrorWords];
     int *where[kErrorWords];
@@ -459,7 +459,8 @@ fa_status fa_device_status(int *where, void *stream) {
         fa::chunk_rows_error_addrs(&w.code[6], &w.where[6]) != cudaSuccess ||
         fa::key_weights_error_addrs(&w.code[7], &w.where[7]) != cudaSuccess ||
         fa::evict_error_addrs(&w.code[8], &w.where[8]) != cudaSuccess ||
-        fa::chunk_tile_error_addrs(&w.code[9], &w.where[9]) != cudaSuccess)
+        fa::chunk_tile_error_addrs(&w.code[9], &w.where[9]) != cudaSuccess ||
+        fa::key_weights_tile_error_addrs(&w.code[10], &w.where[10]) != cudaSuccess)
         return FA_ERR_CUDA;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     status_collect_kernel<<<1, 1, 0, st>>>(w);

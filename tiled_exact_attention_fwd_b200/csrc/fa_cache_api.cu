@@ -266,16 +266,26 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     return done(fa::launch_chunk_tile(D, bf16, causal != 0, tq, tk, tv, p, ctas, cs));
 }
 
+int64_t fa_paged_key_weights_workspace(int Hq, int Hkv, int D, int max_q_len) {
+    if (!heads_ok(Hq, Hkv) || !fa::host_head_dim_ok(D) || max_q_len < 0 || few_rows(Hq / Hkv, max_q_len)) return 0;
+    return static_cast<int64_t>(round256(fa::kChunkMaxCtas * sizeof(fa::ChunkDesc)) +
+                                2 * fa::kChunkMaxCtas * fa::kKeyWeightsPiece * sizeof(float));
+}
+
 fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t *block_table, int max_blocks_per_seq,
                                int page_size, int num_pages, const int32_t *cu_seqlens, const int32_t *kv_lens, int num_seqs,
-                               int total, int max_q_len, const float *lse, float *weights, int64_t width, int Hq, int Hkv,
-                               int D, float scale, int causal, fa_dtype dtype, void *stream) {
+                               int total, int max_q_len, const float *lse, float *weights, int64_t width, void *workspace,
+                               int64_t workspace_bytes, int Hq, int Hkv, int D, float scale, int causal, fa_dtype dtype,
+                               void *stream) {
     fa_status st = chunk_check(max_blocks_per_seq, page_size, num_pages, num_seqs, total, max_q_len, Hq, Hkv, D, dtype);
     if (st != FA_OK) return st;
     if (width < static_cast<int64_t>(max_blocks_per_seq) * page_size) return FA_ERR_SHAPE;
     if (total == 0 || num_seqs == 0) return FA_OK;
-    if (!q || !k_cache || !block_table || !cu_seqlens || !kv_lens || !lse || !weights) return FA_ERR_NULL;
-    if (!aligned(k_cache, 16) || !aligned(lse, 4) || !aligned(weights, 4)) return FA_ERR_ALIGN;
+    const bool few = few_rows(Hq / Hkv, max_q_len);
+    if (!q || !k_cache || !block_table || !cu_seqlens || !kv_lens || !lse || !weights || (!few && !workspace)) return FA_ERR_NULL;
+    if (!few && workspace_bytes < fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len)) return FA_ERR_SHAPE;
+    if (!aligned(k_cache, 16) || !aligned(lse, 4) || !aligned(weights, 4) || (!few && !aligned(workspace, 256)))
+        return FA_ERR_ALIGN;
     fa::ChunkParams p;
     st = chunk_params(p, q, block_table, max_blocks_per_seq, page_size, num_pages, cu_seqlens, kv_lens, num_seqs, total, Hq,
                       Hkv, D, scale);
@@ -286,11 +296,19 @@ fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t
     const int ctas = chunk_ctas();
     if (ctas <= 0) return FA_ERR_CUDA;
     const bool bf16 = dtype == FA_BF16;
-    CUtensorMap tk;
-    if (!fa::host_encode_map(&tk, k_cache, bf16, D, Hkv, static_cast<int64_t>(num_pages) * page_size,
-                             fa::fwd_box_inner_elems(D), fa::key_weights_box(page_size)))
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int inner = fa::fwd_box_inner_elems(D);
+    CUtensorMap tk, tq;
+    if (!fa::host_encode_map(&tk, k_cache, bf16, D, Hkv, static_cast<int64_t>(num_pages) * page_size, inner,
+                             fa::key_weights_box(page_size)))
         return FA_ERR_CUDA;
-    return done(fa::launch_key_weights(D, bf16, causal != 0, tk, p, ctas, static_cast<cudaStream_t>(stream)));
+    if (few) return done(fa::launch_key_weights(D, bf16, causal != 0, tk, p, ctas, cs));
+    p.tile_tokens = 128 / p.G;
+    p.mma_tiles = 1;
+    p.desc = static_cast<fa::ChunkDesc *>(workspace);
+    p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + round256(fa::kChunkMaxCtas * sizeof(fa::ChunkDesc)));
+    if (!fa::host_encode_group_map(&tq, q, bf16, D, p.G, Hkv, total, inner, p.tile_tokens)) return FA_ERR_CUDA;
+    return done(fa::launch_key_weights_tile(D, bf16, causal != 0, tq, tk, p, ctas, cs));
 }
 
 fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_table, int max_blocks_per_seq, int page_size,

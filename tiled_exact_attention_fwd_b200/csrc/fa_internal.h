@@ -186,6 +186,11 @@ cudaError_t launch_key_weights(int D, bool bf16, bool causal, const CUtensorMap 
                                cudaStream_t st);
 int key_weights_box(int page_size);
 cudaError_t key_weights_error_addrs(int **code, int **where);
+// The same on the tensor core (fa_key_weights_tile.cu); p.part_o: kKeyWeightsPiece floats per slot.
+constexpr int kKeyWeightsPiece = 256;
+cudaError_t launch_key_weights_tile(int D, bool bf16, bool causal, const CUtensorMap &tq, const CUtensorMap &tk,
+                                    const ChunkParams &p, int ctas, cudaStream_t st);
+cudaError_t key_weights_tile_error_addrs(int **code, int **where);
 
 // Eviction by accumulated weight (fa_evict.cu).
 struct EvictParams {
