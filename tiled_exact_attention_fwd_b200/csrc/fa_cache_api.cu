@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stdlib.h>
 #include <stdint.h>
 
 #include "fa.h"
@@ -170,7 +171,7 @@ fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const void *k, 
 }
 
 int64_t fa_qk_norm_rope_bwd_workspace(int D) {
-    return fa::host_head_dim_ok(D) ? static_cast<int64_t>(fa::kQkNormBwdCtas) * 2 * D * sizeof(float) : 0;
+    return fa::host_head_dim_ok(D) ? static_cast<int64_t>(fa::kQkNormCtas + 1) * D * sizeof(float) : 0;
 }
 
 fa_status fa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *q_weight,
@@ -333,6 +334,7 @@ fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_tabl
     p.capacity = capacity_of(max_blocks_per_seq, page_size);
     p.Hkv = Hkv; p.D = D;
     p.weights = weights; p.width = width; p.budget = budget; p.recent = recent;
+    if (getenv("EVS")) p.slice = atoi(getenv("EVS"));
     p.kept = kept; p.new_lens = new_lens; p.new_weights = new_weights;
     return done(fa::launch_evict(p, static_cast<cudaStream_t>(stream)));
 }

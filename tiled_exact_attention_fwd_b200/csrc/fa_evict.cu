@@ -29,6 +29,7 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelItems = 4;   // consecutive slots per thread
 constexpr int kHistCopies = 8;
+constexpr int kSelHeld = 16;   // images held in a thread's registers over the passes (the rest is read again)
 
 // Order-preserving image: a > b as floats <=> image(a) > image(b); -0 equals 0, NaN is above +inf.
 __device__ __forceinline__ uint32_t weight_image(float w) {
@@ -85,14 +86,31 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
     uint32_t ties = 0;
     if (k > 0) {
         uint32_t prefix = 0, rank = k;  // the rank-th largest among those that match the prefix
+        uint32_t held[kSelHeld];
+#pragma unroll
+        for (int q = 0; q < kSelHeld; ++q) {
+            const int i = q * kSelThreads + tid;
+            held[q] = i < old ? weight_image(w[i]) : 0u;
+        }
         for (int shift = 24; shift >= 0; shift -= 8) {
             for (int i = tid; i < kHistCopies * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
             __syncthreads();
             uint32_t *mine = hist[(tid >> 5) % kHistCopies];
-            for (int i = tid; i < old; i += kSelThreads) {
-                const uint32_t x = weight_image(w[i]);
-                if (shift == 24 || (x >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&mine[(x >> shift) & 255], 1u);
-            }
+            auto count = [&](uint32_t x, bool valid) {
+                if (shift == 24) {
+                    // the top byte (sign and exponent) takes few values: one addition per value and warp
+                    const uint32_t d = valid ? x >> 24 : 256u;
+                    const uint32_t peers = __match_any_sync(0xffffffffu, d);
+                    if (valid && (threadIdx.x & 31) == __ffs(peers) - 1) atomicAdd(&mine[d], __popc(peers));
+                } else if (valid && (x >> (shift + 8)) == (prefix >> (shift + 8))) {
+                    atomicAdd(&mine[(x >> shift) & 255], 1u);
+                }
+            };
+#pragma unroll
+            for (int q = 0; q < kSelHeld; ++q)
+                if (q * kSelThreads < old) count(held[q], q * kSelThreads + tid < old);
+            for (int i0 = kSelHeld * kSelThreads; i0 < old; i0 += kSelThreads)
+                count(i0 + tid < old ? weight_image(w[i0 + tid]) : 0u, i0 + tid < old);
             __syncthreads();
             if (tid < 32) {  // digits from the largest down: lane l takes digits 255 - 8 l ... 248 - 8 l
                 uint32_t c[8], sum = 0;
@@ -174,12 +192,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 
-// One head's K (first half of blockIdx.x's slices) or V rows, SLICE bytes of each.
+// One head's K (first half of blockIdx.x's slices) or V rows, SLICE bytes of each. In the iteration of
+// chunk c the loads of chunk c + 1 are issued and the places of chunk c + 2 looked up before chunk c is
+// stored.
 template <int SLICE>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int slices) {
     constexpr int LPR = SLICE / 16;               // lanes a row
     constexpr int RPT = kMoveThreads / LPR;       // rows of one load of the CTA
-    constexpr int CHUNK = RPT * kMoveUnroll;
+    constexpr int U = kMoveUnroll, CHUNK = RPT * U;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int b = blockIdx.z, h = blockIdx.y;
     const int n = min(max(p.kv_lens[b], 0), p.capacity);
     if (n <= p.budget) return;
@@ -193,37 +214,76 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     const int32_t *bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks;
     const int r = threadIdx.x / LPR, mask = (1 << p.page_shift) - 1;
     bool bad = false;
-    auto address = [&](int pos) -> uint8_t * {
-        const int pg = __ldg(bt + (pos >> p.page_shift));
-        if (pg < 0 || pg >= p.num_pages) {
-            bad = true;
-            return nullptr;
-        }
-        return pool + ((static_cast<int64_t>(pg) << p.page_shift) + (pos & mask)) * row_bytes;
-    };
-    for (int j0 = 0; j0 < p.budget; j0 += CHUNK) {
-        uint4 v[kMoveUnroll];
-        uint8_t *to[kMoveUnroll];
+    // rows of the pool that chunk j0 moves (to: -1 where nothing moves)
+    auto places = [&](int j0, int *from, int *to) {
+        int src[U];
 #pragma unroll
-        for (int q = 0; q < kMoveUnroll; ++q) {
+        for (int q = 0; q < U; ++q) {
             const int j = j0 + q * RPT + r;
-            to[q] = nullptr;
-            if (j < p.budget) {
-                const int src = kept[j];
-                if (src != j) {
-                    const uint8_t *from = address(src);
-                    to[q] = address(j);
-                    if (from && to[q]) v[q] = *reinterpret_cast<const uint4 *>(from);
-                    else to[q] = nullptr;
+            src[q] = j < p.budget ? __ldg(kept + j) : j;
+        }
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            const int j = j0 + q * RPT + r;
+            from[q] = to[q] = -1;
+            if (src[q] != j) {
+                const int pf = __ldg(bt + (src[q] >> p.page_shift)), pt = __ldg(bt + (j >> p.page_shift));
+                if (pf < 0 || pf >= p.num_pages || pt < 0 || pt >= p.num_pages) {
+                    bad = true;
+                } else {
+                    from[q] = (pf << p.page_shift) + (src[q] & mask);
+                    to[q] = (pt << p.page_shift) + (j & mask);
                 }
             }
         }
-        __syncthreads();  // the chunk is read before any of it is written
+    };
+    int from[U], to[U], nfrom[U], nto[U];
+    uint4 v[U], nv[U];
+    auto fetch = [&](const int *at, uint4 *x) {
 #pragma unroll
-        for (int q = 0; q < kMoveUnroll; ++q)
-            if (to[q]) *reinterpret_cast<uint4 *>(to[q]) = v[q];
+        for (int q = 0; q < U; ++q)
+            if (at[q] >= 0)
+                asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(x[q].x), "=r"(x[q].y), "=r"(x[q].z), "=r"(x[q].w)
+                             : "l"(pool + at[q] * row_bytes)
+                             : "memory");
+    };
+    places(0, from, to);
+    fetch(from, v);
+    places(CHUNK, nfrom, nto);
+    for (int j0 = 0; j0 < p.budget; j0 += CHUNK) {
+        int ffrom[U], fto[U];
+        fetch(nfrom, nv);
+        places(j0 + 2 * CHUNK, ffrom, fto);
+        __syncthreads();  // chunk j0 is read (by all) before any of it is written
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+            if (to[q] >= 0) *reinterpret_cast<uint4 *>(pool + to[q] * row_bytes) = v[q];
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+            v[q] = nv[q];
+            to[q] = nto[q];
+            nfrom[q] = ffrom[q];
+            nto[q] = fto[q];
+        }
     }
     if (bad) record_error(FA_ERR_INDEX, 741);
+}
+
+template <int SLICE>
+cudaError_t launch_move(const EvictParams &p, cudaStream_t st) {
+    const int slices = 2 * p.D * 2 / SLICE;
+    cudaLaunchConfig_t cfg = {};  // waits on the device for the kept slots
+    cfg.gridDim = dim3(slices, p.Hkv, p.batch);
+    cfg.blockDim = dim3(kMoveThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_move_kernel<SLICE>, p, slices);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -232,9 +292,10 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
     evict_select_kernel<<<dim3(p.Hkv, p.batch), kSelThreads, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int slices = 2 * p.D * 2 / 64;
-    evict_move_kernel<64><<<dim3(slices, p.Hkv, p.batch), kMoveThreads, 0, st>>>(p, slices);
-    return cudaGetLastError();
+    const int which = p.slice ? p.slice : 64;
+    if (which >= 256 && p.D >= 128) return launch_move<256>(p, st);
+    if (which >= 128 && p.D >= 64) return launch_move<128>(p, st);
+    return launch_move<64>(p, st);
 }
 
 cudaError_t evict_error_addrs(int **code, int **where) { return device_error_addrs(code, where); }

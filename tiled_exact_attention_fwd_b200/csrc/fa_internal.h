@@ -125,7 +125,7 @@ struct QkNormParams {
     int64_t q_out_stride, k_out_stride;
     const void *dq_out, *dk_out;                // backward: gradients of q_out, k_out
     int64_t dq_out_stride, dk_out_stride;
-    float *partials, *dwq, *dwk;                // backward: (kQkNormBwdCtas, 2, D) workspace; weight gradients
+    float *partials, *dwq, *dwk;                // backward: (kQkNormCtas + 1, D) workspace; weight gradients
     int64_t n;                                  // tokens
     int Hq, Hk;
     float eps;
@@ -133,9 +133,10 @@ struct QkNormParams {
     const int32_t *cu_seqlens, *kv_lens, *block_table;
     int num_seqs, max_blocks, page_shift, num_pages;
     // set by the launcher
-    int heads_per_warp, q_units, k_units, units_per_token;
+    int heads_per_warp, q_units, k_units;       // heads of a work unit, units a token
+    int ctas_q, ctas_k;                         // CTAs of the q rows, of the k rows (and again of the v rows)
 };
-constexpr int kQkNormBwdCtas = 592;
+constexpr int kQkNormCtas = 296;                // of a whole launch (two an SM), give or take one
 cudaError_t launch_qk_norm(int D, bool bf16, bool interleaved, bool backward, const QkNormParams &p, cudaStream_t st);
 cudaError_t qk_norm_error_addrs(int **code, int **where);
 
@@ -201,6 +202,7 @@ struct EvictParams {
     const float *weights;                       // (batch, Hkv, width)
     int64_t width;
     int budget, recent;
+    int slice;
     int32_t *kept, *new_lens;                   // (batch, Hkv, budget), (batch)
     float *new_weights;                         // as weights
 };

@@ -13,8 +13,8 @@
 //
 // Everything is bytes: each row is read once and written once (backward: x and dy read, dx
 // written), a 16-byte vector per lane, a row on D / 8 neighbouring lanes, so a row's sums are
-// log2(D / 8) shuffles. A warp takes one token and a chunk of consecutive heads, UNROLL rows a
-// lane at a time so that several loads are in flight. All arithmetic is 32-bit; an output is
+// log2(D / 8) shuffles. Two CTAs an SM walk over the tokens, each warp with the next rows in flight
+// while it works on the current ones. All arithmetic is 32-bit; an output is
 // rounded once. The weight gradients are summed in registers, then over the CTA's warps in
 // shared memory, then over the CTAs by a second launch in a fixed order (no atomics: the same
 // inputs give the same bits).
@@ -139,96 +139,158 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// A token's row of the angle table; a position outside it is reported and row 0 read instead
-// (that output is wrong, but nothing outside the table is read).
-__device__ __forceinline__ const float *angle_row(const QkNormParams &p, int64_t pos, int lane) {
+// A token's row of the angle table; a position outside it sets `bad` (reported at the kernel's end: a
+// call here would hold back the loads around it) and row 0 is read instead (that output is wrong, but
+// nothing outside the table is read).
+__device__ __forceinline__ const float *angle_row(const QkNormParams &p, int64_t pos, bool &bad) {
     if (pos < 0 || pos >= p.max_pos) {
-        if (lane == 0) record_error(FA_ERR_INDEX, 700);
+        bad = true;
         pos = 0;
     }
     return p.cos_sin + pos * p.rot;
 }
 
-// Work unit: one token and up to p.heads_per_warp consecutive heads of q, of k, or (paged) of v.
-// PAGED: k and v rows go to the token's slot in the pages.
-template <int D, bool BF16, bool INTER, bool PAGED, int UNROLL>
-__global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(const QkNormParams p) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes a row, rows an iteration
-    const int lane = threadIdx.x & 31, sub = lane % LPR, row_in = lane / LPR;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t tok = unit / p.units_per_token;
-    if (tok >= p.n) return;
-    int u = static_cast<int>(unit - tok * p.units_per_token);
-    const int kind = u < p.q_units ? 0 : (u < p.q_units + p.k_units ? 1 : 2);
-    u -= kind == 0 ? 0 : (kind == 1 ? p.q_units : p.q_units + p.k_units);
-    const int heads = kind == 0 ? p.Hq : p.Hk;
-    const int h0 = u * p.heads_per_warp, h1 = min(heads, h0 + p.heads_per_warp);
+// Rows are read once: not kept in L1. (Not the read-only path: the output may be the input.)
+__device__ __forceinline__ uint4 ld_row(const uint16_t *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 
-    const uint16_t *x = static_cast<const uint16_t *>(kind == 0 ? p.q : (kind == 1 ? p.k : p.v)) +
-                        tok * (kind == 0 ? p.q_stride : (kind == 1 ? p.k_stride : p.v_stride));
-    uint16_t *y = nullptr;
-    int64_t pos = 0;
-    if (PAGED) {
-        const int total = p.cu_seqlens[p.num_seqs];
-        if (tok < p.cu_seqlens[0] || tok >= total) return;  // rows of no sequence stay as they are
-        const int b = warp_seq_of_token(p.cu_seqlens, p.num_seqs, static_cast<int>(tok), lane);
-        const int64_t slot = static_cast<int64_t>(p.kv_lens[b]) - p.cu_seqlens[b + 1] + tok;
-        pos = p.positions ? p.positions[tok] : slot;
-        if (kind == 0) {
-            y = static_cast<uint16_t *>(p.q_out) + tok * p.q_out_stride;
+// The kinds of rows (q, k, paged: v) have CTAs of their own: CTA blockIdx.x is number `cta` of `ctas` of
+// its kind.
+struct Share {
+    int kind, cta, ctas;
+    __device__ __forceinline__ explicit Share(const QkNormParams &p) {
+        const int x = blockIdx.x;
+        kind = x < p.ctas_q ? 0 : (x < p.ctas_q + p.ctas_k ? 1 : 2);
+        cta = x - (kind == 0 ? 0 : (kind == 1 ? p.ctas_q : p.ctas_q + p.ctas_k));
+        ctas = kind == 0 ? p.ctas_q : (kind == 1 ? p.ctas_k : static_cast<int>(gridDim.x) - p.ctas_q - p.ctas_k);
+    }
+};
+
+// A warp's walk over the work units of its kind: a unit is one token and up to p.heads_per_warp
+// consecutive heads, worked on in batches of BATCH heads. The next batch is asked for before the current
+// one is worked on, a unit's angles a batch before it begins, and its position a unit before that, so
+// that the loads that depend on one another are never waited for in a row.
+struct Walk {
+    int64_t unit, units, step, tok, ahead;  // ahead: position of the unit after the current one
+    int per_token, heads, hb, h1;
+    __device__ __forceinline__ Walk(const QkNormParams &p, const Share &sh) {
+        per_token = sh.kind == 0 ? p.q_units : p.k_units;
+        heads = sh.kind == 0 ? p.Hq : p.Hk;
+        units = p.n * per_token;
+        step = static_cast<int64_t>(sh.ctas) * kWarps;
+        unit = static_cast<int64_t>(sh.cta) * kWarps + (threadIdx.x >> 5);
+        ahead = p.positions && unit < units ? p.positions[unit / per_token] : 0;
+    }
+    // takes unit `unit`; its position
+    __device__ __forceinline__ int64_t enter(const QkNormParams &p) {
+        tok = unit / per_token;
+        hb = static_cast<int>(unit - tok * per_token) * p.heads_per_warp;
+        h1 = min(heads, hb + p.heads_per_warp);
+        const int64_t pos = ahead;
+        if (p.positions && unit + step < units) ahead = p.positions[(unit + step) / per_token];
+        return pos;
+    }
+};
+
+constexpr int kFwdRows = 4, kBwdRows = 2;  // rows a lane takes at a time
+
+// PAGED: k and v rows go to the token's slot in the pages.
+template <int D, bool BF16, bool INTER, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_fwd_kernel(const QkNormParams p) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, U = kFwdRows, BATCH = RPI * U;  // lanes a row, rows of a load
+    const int lane = threadIdx.x & 31, sub = lane % LPR, row_in = lane / LPR;
+    const Share sh(p);
+    const int kind = sh.kind;
+    const uint16_t *x0 = static_cast<const uint16_t *>(kind == 0 ? p.q : (kind == 1 ? p.k : p.v)) + sub * 8;
+    const int64_t xs = kind == 0 ? p.q_stride : (kind == 1 ? p.k_stride : p.v_stride);
+    bool bad = false, lost = false;
+    Walk w(p, sh);
+    // where token w.tok's row of heads goes (PAGED: null where it has no place), and its position
+    auto place = [&](int64_t &pos) -> uint16_t * {
+        if constexpr (!PAGED) {
+            return static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) +
+                   w.tok * (kind == 0 ? p.q_out_stride : p.k_out_stride) + sub * 8;
         } else {
+            // rows of no sequence stay as they are
+            if (w.tok < p.cu_seqlens[0] || w.tok >= p.cu_seqlens[p.num_seqs]) return nullptr;
+            const int b = warp_seq_of_token(p.cu_seqlens, p.num_seqs, static_cast<int>(w.tok), lane);
+            if (b < 0 || b >= p.num_seqs) return nullptr;  // offsets that do not rise
+            const int64_t slot = static_cast<int64_t>(p.kv_lens[b]) - p.cu_seqlens[b + 1] + w.tok;
+            if (!p.positions) pos = slot;
+            if (kind == 0) return static_cast<uint16_t *>(p.q_out) + w.tok * p.q_out_stride + sub * 8;
             int pg = -1;
             if (slot >= 0 && slot < (static_cast<int64_t>(p.max_blocks) << p.page_shift))
                 pg = p.block_table[static_cast<int64_t>(b) * p.max_blocks + (slot >> p.page_shift)];
             if (pg < 0 || pg >= p.num_pages) {  // no place for this token: reported, nothing written
-                if (lane == 0) record_error(FA_ERR_INDEX, 701);
-                return;
+                lost = true;
+                return nullptr;
             }
             const int64_t row = (static_cast<int64_t>(pg) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-            y = static_cast<uint16_t *>(kind == 1 ? p.k_out : p.v_out) + row * p.Hk * D;
+            return static_cast<uint16_t *>(kind == 1 ? p.k_out : p.v_out) + row * p.Hk * D + sub * 8;
         }
-    } else {
-        pos = p.positions[tok];
-        y = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) + tok * (kind == 0 ? p.q_out_stride : p.k_out_stride);
-    }
-
-    if (PAGED && kind == 2) {  // values: a copy
-        for (int h = h0 + row_in; h < h1; h += RPI * UNROLL) {
-            uint4 v[UNROLL];
+    };
+    auto load = [&](uint4 *v) {
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i)
-                if (h + i * RPI < h1) v[i] = *reinterpret_cast<const uint4 *>(x + (h + i * RPI) * D + sub * 8);
-#pragma unroll
-            for (int i = 0; i < UNROLL; ++i)
-                if (h + i * RPI < h1) *reinterpret_cast<uint4 *>(y + (h + i * RPI) * D + sub * 8) = v[i];
+        for (int i = 0; i < U; ++i) {
+            const int h = w.hb + i * RPI + row_in;
+            v[i] = h < w.h1 ? ld_row(x0 + w.tok * xs + h * D) : make_uint4(0, 0, 0, 0);
         }
-        return;
-    }
-
+    };
     const Turn<D, INTER> turn(lane, p.rot);
-    float a[8], b[8];  // y_i = r (x_i a_i + x_p b_i)
-    {
-        const void *w = kind == 0 ? p.wq : p.wk;
-        float c[8], s[8], wi[8], wp[8];
-        turn.angles(angle_row(p, pos, lane), p.rot, lane, 1.f, c, s);
-        load_weights<BF16>(w, p.w32, sub * 8, wi);
-        load_weights<BF16>(w, p.w32, turn.pe, wp);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            a[i] = wi[i] * c[i];
-            b[i] = wp[INTER ? (i ^ 1) : i] * s[i];
-        }
+    const void *wt = kind == 0 ? p.wq : p.wk;
+    float wi[8], wp[8];
+    if (kind < 2) {
+        load_weights<BF16>(wt, p.w32, sub * 8, wi);
+        load_weights<BF16>(wt, p.w32, turn.pe, wp);
     }
-    for (int hb = h0; hb < h1; hb += RPI * UNROLL) {
-        uint4 v[UNROLL];
+    uint4 v[U];
+    float c[8], s[8], a[8], b[8];  // angles of the unit to come; y_i = r (x_i a_i + x_p b_i)
+    bool more = w.unit < w.units, fresh = true;
+    uint16_t *y = nullptr;
+    if (more) {
+        int64_t pos = w.enter(p);
+        load(v);
+        y = place(pos);
+        if (kind < 2) turn.angles(angle_row(p, pos, bad), p.rot, lane, 1.f, c, s);
+    }
+#pragma unroll 1
+    while (more) {
+        if (fresh && kind < 2) {
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
-            const int h = hb + i * RPI + row_in;
-            v[i] = h < h1 ? *reinterpret_cast<const uint4 *>(x + h * D + sub * 8) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 8; ++i) {
+                a[i] = wi[i] * c[i];
+                b[i] = wp[INTER ? (i ^ 1) : i] * s[i];
+            }
+        }
+        const int hb = w.hb, h1 = w.h1;
+        uint16_t *const dst = y;
+        uint4 nv[U];
+        w.hb += BATCH;
+        fresh = w.hb >= w.h1;
+        if (fresh) {
+            w.unit += w.step;
+            more = w.unit < w.units;
+            if (more) {
+                int64_t pos = w.enter(p);
+                load(nv);
+                y = place(pos);
+                if (kind < 2) turn.angles(angle_row(p, pos, bad), p.rot, lane, 1.f, c, s);
+            }
+        } else {
+            load(nv);
         }
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) {
+        for (int i = 0; i < U; ++i) {
             const int h = hb + i * RPI + row_in;
+            if (PAGED && kind == 2) {  // values: a copy
+                if (dst && h < h1) *reinterpret_cast<uint4 *>(dst + h * D) = v[i];
+                continue;
+            }
             float xi[8], xp[8], out[8];
             unpack8<BF16>(v[i], xi);
             if (INTER) {
@@ -240,143 +302,199 @@ __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(const QkNormParam
             float ss = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) ss = fmaf(xi[k], xi[k], ss);
-            const float r = 1.0f / sqrtf(row_sum<LPR>(ss) * (1.0f / D) + p.eps);
+            const float r = rsqrtf(row_sum<LPR>(ss) * (1.0f / D) + p.eps);
 #pragma unroll
             for (int k = 0; k < 8; ++k) out[k] = r * fmaf(xi[k], a[k], xp[k] * b[k]);
-            if (h < h1) *reinterpret_cast<uint4 *>(y + h * D + sub * 8) = pack8<BF16>(out);
+            if (dst && h < h1) *reinterpret_cast<uint4 *>(dst + h * D) = pack8<BF16>(out);
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = nv[i];
     }
+    if (bad && lane == 0) record_error(FA_ERR_INDEX, 700);
+    if (lost && lane == 0) record_error(FA_ERR_INDEX, 701);
 }
 
-// Backward: a fixed grid of p.grid CTAs, each warp walking units gridDim.x * kWarps apart, first
-// those of q, then those of k, adding g x r of its rows to eight weight-gradient sums a lane.
-template <int D, bool BF16, bool INTER, int UNROLL>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const QkNormParams p) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR;
+// Backward: the same walk over x and dy, adding g x r of each row to eight weight-gradient sums a lane.
+template <int D, bool BF16, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkNormParams p) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, U = kBwdRows, BATCH = RPI * U;
     __shared__ float part[kWarps][D];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, row_in = lane / LPR;
     const Turn<D, INTER> turn(lane, p.rot);
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int kind = 0; kind < 2; ++kind) {
-        const int heads = kind == 0 ? p.Hq : p.Hk, per_token = kind == 0 ? p.q_units : p.k_units;
-        const void *w = kind == 0 ? p.wq : p.wk;
-        float wi[8], dw[8];
-        load_weights<BF16>(w, p.w32, sub * 8, wi);
+    const Share sh(p);
+    const int kind = sh.kind;
+    const uint16_t *x0 = static_cast<const uint16_t *>(kind == 0 ? p.q : p.k) + sub * 8;
+    const uint16_t *dy0 = static_cast<const uint16_t *>(kind == 0 ? p.dq_out : p.dk_out) + sub * 8;
+    uint16_t *dx0 = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) + sub * 8;
+    const int64_t xs = kind == 0 ? p.q_stride : p.k_stride, dys = kind == 0 ? p.dq_out_stride : p.dk_out_stride;
+    const int64_t dxs = kind == 0 ? p.q_out_stride : p.k_out_stride;
+    bool bad = false;
+    Walk w(p, sh);
+    float wi[8], dw[8];
+    load_weights<BF16>(kind == 0 ? p.wq : p.wk, p.w32, sub * 8, wi);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dw[k] = 0.f;
-        for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < p.n * per_token; unit += step) {
-            const int64_t tok = unit / per_token;
-            const int h0 = static_cast<int>(unit - tok * per_token) * p.heads_per_warp;
-            const int h1 = min(heads, h0 + p.heads_per_warp);
-            const uint16_t *x = static_cast<const uint16_t *>(kind == 0 ? p.q : p.k) + tok * (kind == 0 ? p.q_stride : p.k_stride);
-            const uint16_t *dy = static_cast<const uint16_t *>(kind == 0 ? p.dq_out : p.dk_out) +
-                                 tok * (kind == 0 ? p.dq_out_stride : p.dk_out_stride);
-            uint16_t *dx = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) +
-                           tok * (kind == 0 ? p.q_out_stride : p.k_out_stride);
-            float c[8], s[8];
-            turn.angles(angle_row(p, p.positions[tok], lane), p.rot, lane, -1.f, c, s);
-            for (int hb = h0; hb < h1; hb += RPI * UNROLL) {
-                uint4 vx[UNROLL], vy[UNROLL];
+    for (int k = 0; k < 8; ++k) dw[k] = 0.f;
+    auto load = [&](uint4 *ox, uint4 *oy) {
 #pragma unroll
-                for (int i = 0; i < UNROLL; ++i) {
-                    const int h = hb + i * RPI + row_in;
-                    vx[i] = h < h1 ? *reinterpret_cast<const uint4 *>(x + h * D + sub * 8) : make_uint4(0, 0, 0, 0);
-                    vy[i] = h < h1 ? *reinterpret_cast<const uint4 *>(dy + h * D + sub * 8) : make_uint4(0, 0, 0, 0);
-                }
+        for (int i = 0; i < U; ++i) {
+            const int h = w.hb + i * RPI + row_in;
+            ox[i] = h < w.h1 ? ld_row(x0 + w.tok * xs + h * D) : make_uint4(0, 0, 0, 0);
+            oy[i] = h < w.h1 ? ld_row(dy0 + w.tok * dys + h * D) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    uint4 vx[U], vy[U];
+    float c[8], s[8], nc[8], ns[8];
+    bool more = w.unit < w.units, fresh = true;
+    if (more) {
+        const int64_t pos = w.enter(p);
+        load(vx, vy);
+        turn.angles(angle_row(p, pos, bad), p.rot, lane, -1.f, nc, ns);
+    }
+#pragma unroll 1
+    while (more) {
+        if (fresh) {
 #pragma unroll
-                for (int i = 0; i < UNROLL; ++i) {
-                    const int h = hb + i * RPI + row_in;
-                    float xi[8], yi[8], yp[8], u[8];
-                    unpack8<BF16>(vx[i], xi);
-                    unpack8<BF16>(vy[i], yi);
-                    if (INTER) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) yp[k] = yi[k ^ 1];
-                    } else {
-                        unpack8<BF16>(shfl4(vy[i], turn.src), yp);
-                    }
-                    float ss = 0.f, t = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        u[k] = fmaf(yi[k], c[k], yp[k] * s[k]);  // g = R^T dy
-                        ss = fmaf(xi[k], xi[k], ss);
-                        t = fmaf(u[k] * wi[k], xi[k], t);
-                    }
-                    ss = row_sum<LPR>(ss);
-                    t = row_sum<LPR>(t);
-                    const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-                    const float q = r * r * t * (1.0f / D);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (h < h1) dw[k] = fmaf(u[k], xi[k] * r, dw[k]);
-                        u[k] = r * (u[k] * wi[k] - xi[k] * q);
-                    }
-                    if (h < h1) *reinterpret_cast<uint4 *>(dx + h * D + sub * 8) = pack8<BF16>(u);
-                }
+            for (int i = 0; i < 8; ++i) {
+                c[i] = nc[i];
+                s[i] = ns[i];
             }
         }
-        if (!p.partials) continue;
-        // the rows of a warp, then the CTA's warps, in a fixed order
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int o = LPR; o < 32; o <<= 1) dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
-        if (row_in == 0)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) part[warp][sub * 8 + k] = dw[k];
-        __syncthreads();
-        for (int e = threadIdx.x; e < D; e += kThreads) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) sum += part[i][e];
-            p.partials[(static_cast<int64_t>(blockIdx.x) * 2 + kind) * D + e] = sum;
+        const int hb = w.hb, h1 = w.h1;
+        uint16_t *const dx = dx0 + w.tok * dxs;
+        uint4 nx[U], ny[U];
+        w.hb += BATCH;
+        fresh = w.hb >= w.h1;
+        if (fresh) {
+            w.unit += w.step;
+            more = w.unit < w.units;
+            if (more) {
+                const int64_t pos = w.enter(p);
+                load(nx, ny);
+                turn.angles(angle_row(p, pos, bad), p.rot, lane, -1.f, nc, ns);
+            }
+        } else {
+            load(nx, ny);
         }
-        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int h = hb + i * RPI + row_in;
+            float xi[8], yi[8], yp[8], u[8];
+            unpack8<BF16>(vx[i], xi);
+            unpack8<BF16>(vy[i], yi);
+            if (INTER) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) yp[k] = yi[k ^ 1];
+            } else {
+                unpack8<BF16>(shfl4(vy[i], turn.src), yp);
+            }
+            float ss = 0.f, t = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                u[k] = fmaf(yi[k], c[k], yp[k] * s[k]);  // g = R^T dy
+                ss = fmaf(xi[k], xi[k], ss);
+                t = fmaf(u[k] * wi[k], xi[k], t);
+            }
+            ss = row_sum<LPR>(ss);
+            t = row_sum<LPR>(t);
+            const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+            const float q = r * r * t * (1.0f / D);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (h < h1) dw[k] = fmaf(u[k], xi[k] * r, dw[k]);
+                u[k] = r * (u[k] * wi[k] - xi[k] * q);
+            }
+            if (h < h1) *reinterpret_cast<uint4 *>(dx + h * D) = pack8<BF16>(u);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            vx[i] = nx[i];
+            vy[i] = ny[i];
+        }
+    }
+    if (bad && lane == 0) record_error(FA_ERR_INDEX, 700);
+    if (!p.partials) return;
+    // the rows of a warp, then the CTA's warps, in a fixed order
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
+    if (row_in == 0)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) part[warp][sub * 8 + k] = dw[k];
+    __syncthreads();
+    for (int e = threadIdx.x; e < D; e += kThreads) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) sum += part[i][e];
+        p.partials[static_cast<int64_t>(blockIdx.x) * D + e] = sum;
     }
 }
 
-// dw[kind][e] = sum over the CTAs' partials: 32 columns a block, 8 CTA slices a column.
-__global__ void __launch_bounds__(kThreads) qk_norm_dw_kernel(const float *partials, int ctas, int D, float *dwq, float *dwk) {
-    __shared__ float s[kWarps][32];
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;  // of 2 * D
+// The weights' gradients: blockIdx.y 0 sums the partials of the q CTAs, 1 those of the k CTAs; 32 columns
+// a block, 32 slices of the CTAs a column.
+__global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const QkNormParams p, int D) {
+    __shared__ float s[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    const int c0 = blockIdx.y == 0 ? 0 : p.ctas_q, c1 = c0 + (blockIdx.y == 0 ? p.ctas_q : p.ctas_k);
     float sum = 0.f;
-    for (int c = slice; c < ctas; c += kWarps) sum += partials[static_cast<int64_t>(c) * 2 * D + col];
+#pragma unroll 4
+    for (int c = c0 + slice; c < c1; c += 32) sum += p.partials[static_cast<int64_t>(c) * D + col];
     s[slice][lane] = sum;
     __syncthreads();
     if (slice == 0) {
         sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) sum += s[i][lane];
-        float *out = col < D ? dwq : dwk;
-        if (out) out[col < D ? col : col - D] = sum;
+        for (int i = 0; i < 32; ++i) sum += s[i][lane];
+        float *out = blockIdx.y == 0 ? p.dwq : p.dwk;
+        if (out) out[col] = sum;
     }
 }
 
 template <int D, bool BF16, bool INTER>
 cudaError_t launch_d(bool backward, QkNormParams p, cudaStream_t st) {
     constexpr int RPI = 32 / (D / 8);
-    // 4 rows a lane in flight forward, 2 (of x and dy each) backward
-    p.heads_per_warp = RPI * (backward ? 2 : 4);
-    p.q_units = (p.Hq + p.heads_per_warp - 1) / p.heads_per_warp;
-    p.k_units = (p.Hk + p.heads_per_warp - 1) / p.heads_per_warp;
+    const int batch = RPI * (backward ? kBwdRows : kFwdRows);  // heads a warp works on at a time
+    const bool paged = p.cu_seqlens != nullptr;
+    // Two CTAs an SM, shared out by the kinds' heads. A unit is one batch while that leaves CTAs idle, else
+    // up to four batches of a token, which share its angles.
+    const int most = kQkNormCtas;
+    auto units = [&](int heads, int per) { return static_cast<int64_t>((heads + per - 1) / per); };
+    const int heads = p.Hq + p.Hk * (paged ? 2 : 1);
+    p.heads_per_warp = batch;
+    if (p.n * (units(p.Hq, batch) + units(p.Hk, batch) * (paged ? 2 : 1)) > static_cast<int64_t>(most) * kWarps * 4)
+        p.heads_per_warp = 4 * batch;
+    p.q_units = static_cast<int>(units(p.Hq, p.heads_per_warp));
+    p.k_units = static_cast<int>(units(p.Hk, p.heads_per_warp));
+    auto share = [&](int of_heads, int per_token) {
+        const int64_t need = (p.n * per_token + kWarps - 1) / kWarps;
+        int64_t mine = static_cast<int64_t>(most) * of_heads / heads;
+        if (mine < 1) mine = 1;
+        return static_cast<int>(need < mine ? need : mine);
+    };
+    p.ctas_q = share(p.Hq, p.q_units);
+    p.ctas_k = share(p.Hk, p.k_units);
+    const int grid = p.ctas_q + p.ctas_k + (paged ? p.ctas_k : 0);
     if (backward) {
-        const int64_t most = (p.n * (p.q_units > p.k_units ? p.q_units : p.k_units) + kWarps - 1) / kWarps;
-        const int grid = static_cast<int>(most < kQkNormBwdCtas ? most : kQkNormBwdCtas);
-        qk_norm_bwd_kernel<D, BF16, INTER, 2><<<grid, kThreads, 0, st>>>(p);
+        qk_norm_bwd_kernel<D, BF16, INTER><<<grid, kThreads, 0, st>>>(p);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || !p.partials) return e;
-        qk_norm_dw_kernel<<<2 * D / 32, kThreads, 0, st>>>(p.partials, grid, D, p.dwq, p.dwk);
-        return cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};  // waits on the device for the kernel above
+        cfg.gridDim = dim3(D / 32, 2, 1);
+        cfg.blockDim = dim3(1024, 1, 1);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, qk_norm_dw_kernel, p, D);
+        return e != cudaSuccess ? e : cudaGetLastError();
     }
-    const bool paged = p.cu_seqlens != nullptr;
-    p.units_per_token = p.q_units + p.k_units * (paged ? 2 : 1);
-    const int64_t grid = (p.n * p.units_per_token + kWarps - 1) / kWarps;
-    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (paged)
-        qk_norm_fwd_kernel<D, BF16, INTER, true, 4><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p);
+        qk_norm_fwd_kernel<D, BF16, INTER, true><<<grid, kThreads, 0, st>>>(p);
     else
-        qk_norm_fwd_kernel<D, BF16, INTER, false, 4><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p);
+        qk_norm_fwd_kernel<D, BF16, INTER, false><<<grid, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
