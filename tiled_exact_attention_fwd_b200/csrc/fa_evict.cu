@@ -112,31 +112,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             for (int i0 = kSelHeld * kSelThreads; i0 < old; i0 += kSelThreads)
                 count(i0 + tid < old ? weight_image(w[i0 + tid]) : 0u, i0 + tid < old);
             __syncthreads();
-            if (tid < 32) {  // digits from the largest down: lane l takes digits 255 - 8 l ... 248 - 8 l
-                uint32_t c[8], sum = 0;
+            if (tid < 256) {  // thread d takes digit 255 - d: ranks from the largest digit down
+                uint32_t c = 0;
 #pragma unroll
-                for (int d = 0; d < 8; ++d) {
-                    c[d] = 0;
-#pragma unroll
-                    for (int q = 0; q < kHistCopies; ++q) c[d] += hist[q][255 - 8 * tid - d];
-                    sum += c[d];
-                }
-                uint32_t incl = sum;
+                for (int q = 0; q < kHistCopies; ++q) c += hist[q][255 - tid];
+                uint32_t incl = c;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (tid >= o) incl += x;
+                    if ((tid & 31) >= o) incl += x;
                 }
-                uint32_t before = incl - sum;
-                if (before < rank && rank <= incl) {
-#pragma unroll
-                    for (int d = 0; d < 8; ++d) {
-                        if (before < rank && rank <= before + c[d]) {
-                            s_digit = 255 - 8 * tid - d;
-                            s_rank = rank - before;
-                        }
-                        before += c[d];
-                    }
+                if ((tid & 31) == 31) warp_sums[tid >> 5] = incl;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                for (int i = 0; i < (tid >> 5); ++i) incl += warp_sums[i];
+                if (incl - c < rank && rank <= incl) {
+                    s_digit = 255 - tid;
+                    s_rank = rank - (incl - c);
                 }
             }
             __syncthreads();

@@ -136,7 +136,7 @@ struct QkNormParams {
     int heads_per_warp, q_units, k_units;       // heads of a work unit, units a token
     int ctas_q, ctas_k;                         // CTAs of the q rows, of the k rows (and again of the v rows)
 };
-constexpr int kQkNormCtas = 296;                // of a whole launch (two an SM), give or take one
+constexpr int kQkNormCtas = 296;                // most of a launch (two an SM), give or take one
 cudaError_t launch_qk_norm(int D, bool bf16, bool interleaved, bool backward, const QkNormParams &p, cudaStream_t st);
 cudaError_t qk_norm_error_addrs(int **code, int **where);
 

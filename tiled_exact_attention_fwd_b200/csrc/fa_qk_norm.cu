@@ -3,21 +3,20 @@
 // (fa_qk_norm_rope_paged), and the gradients (fa_qk_norm_rope_bwd).
 //
 // Mathematics, for one head row x of D values, weights w, and the token's angles (c, s):
-//   r = 1 / sqrt(mean(x^2) + eps),  n = w * x * r,  y = R n,
+//   r = 1 / sqrt(mean(x^2) + eps),  n = w x r,  y = R n,
 //   R turns the pairs (a, b) of the first `rot` values: (a c - b s, b c + a s); a pair is (i,
-//   i + rot/2), or (2i, 2i + 1) when interleaved. With a_i = w_i c_i and b_i = -+ w_p s_i (p the
-//   other half of the pair) the row is y_i = r (x_i a_i + x_p b_i): the weights and angles are
-//   multiplied together once per token and stay in registers for its heads.
+//   i + rot/2), or (2i, 2i + 1) when interleaved. (r is the row's, so it is multiplied in last.)
 // Backward: g = R^T dy (the angles turned back), u = w g, t = sum(u x),
 //   dx = r u - x r^3 t / D,  dw = sum over tokens and heads of g x r.
 //
 // Everything is bytes: each row is read once and written once (backward: x and dy read, dx
-// written), a 16-byte vector per lane, a row on D / 8 neighbouring lanes, so a row's sums are
-// log2(D / 8) shuffles. Two CTAs an SM walk over the tokens, each warp with the next rows in flight
-// while it works on the current ones. All arithmetic is 32-bit; an output is
-// rounded once. The weight gradients are summed in registers, then over the CTA's warps in
-// shared memory, then over the CTAs by a second launch in a fixed order (no atomics: the same
-// inputs give the same bits).
+// written). A lane takes two 16-byte chunks of a row, chosen so that both halves of each pair are
+// its own (Turn): no exchange but the row's sum, log2(D / 16) shuffles, and all arithmetic in pairs of
+// floats (with a chunk a lane, and the partners' values by shuffles, the instructions took as long as the
+// bytes). Two CTAs an SM walk over the tokens, each warp with the rows of three batches in flight while it
+// works on one. All arithmetic is 32-bit; an output is rounded once. The weight gradients are summed in
+// registers, then over the CTA's warps in shared memory, then over the CTAs by a second launch in a
+// fixed order (no atomics: the same inputs give the same bits).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -37,103 +36,191 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
+// Eight 16-bit values as four pairs of floats, and back (one rounding).
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4 &v, float *f) {
+__device__ __forceinline__ void unpack8(const uint4 &v, uint64_t *f) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (BF16) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            f[i] = f2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
         } else {
             const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
-            f[2 * i] = t.x;
-            f[2 * i + 1] = t.y;
+            f[i] = f2(t.x, t.y);
         }
     }
 }
-
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float *f) {
+__device__ __forceinline__ uint4 pack8(const uint64_t *f) {
     uint4 v;
     uint32_t *u = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = BF16 ? pack2_bf16(f[2 * i], f[2 * i + 1]) : pack2_f16(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_split(f[i], lo, hi);
+        u[i] = BF16 ? pack2_bf16(lo, hi) : pack2_f16(lo, hi);
+    }
     return v;
-}
-
-__device__ __forceinline__ uint4 shfl4(const uint4 &v, int src) {
-    uint4 o;
-    o.x = __shfl_sync(0xffffffffu, v.x, src);
-    o.y = __shfl_sync(0xffffffffu, v.y, src);
-    o.z = __shfl_sync(0xffffffffu, v.z, src);
-    o.w = __shfl_sync(0xffffffffu, v.w, src);
-    return o;
 }
 
 // Eight weights from element e on (ones where there are none).
 template <bool BF16>
-__device__ __forceinline__ void load_weights(const void *w, int w32, int e, float *f) {
+__device__ __forceinline__ void load_weights(const void *w, int w32, int e, uint64_t *f) {
     if (!w) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 1.f;
+        for (int i = 0; i < 4; ++i) f[i] = f2(1.f, 1.f);
     } else if (w32) {
         const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + e);
         const float4 a = __ldg(p), b = __ldg(p + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        f[0] = f2(a.x, a.y);
+        f[1] = f2(a.z, a.w);
+        f[2] = f2(b.x, b.y);
+        f[3] = f2(b.z, b.w);
     } else {
         unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + e)), f);
     }
 }
 
-// How this lane's eight values (elements [e, e + 8) of a row) are turned.
+// A lane's part of a row: the 8-value chunks that begin at elements A and B, chosen so that both halves of
+// every pair lie in one lane: of the turned part, chunk i and chunk i + rot/16; of the rest, neighbours.
 template <int D, bool INTER>
 struct Turn {
-    static constexpr int LPR = D / 8;  // lanes per row
-    int src;                           // lane that holds the other halves of the pairs (itself when in-lane or not turned)
-    int pe;                            // first element of that lane
-    bool turned, upper;                // any element turned; elements are second halves (INTER: neither)
+    static constexpr int LPR = D / 16;  // lanes per row
+    int A, B;
+    bool turned;
+    // Half pairs: cosine and sine of A's elements (and B's) in pairs. Neighbouring pairs: cosine and sine of A's
+    // four pairs, then B's.
+    uint64_t c[4], s[4];
     __device__ __forceinline__ Turn(int lane, int rot) {
-        const int sub = lane % LPR, e = sub * 8, hl = rot / 16;  // half of the turned part in lanes
-        turned = e < rot;
-        upper = !INTER && turned && e >= rot / 2;
-        src = (INTER || !turned) ? lane : (upper ? lane - hl : lane + hl);
-        pe = (INTER || !turned) ? e : (upper ? e - rot / 2 : e + rot / 2);
+        const int l = lane % LPR, half = rot / 16;
+        turned = l < half;
+        A = turned ? l * 8 : rot + (l - half) * 16;
+        B = turned ? A + rot / 2 : A + 8;
     }
-    // cos and signed sin of each element: y_i = c_i x_i + s_i x_p (sign -1: turned back)
-    __device__ __forceinline__ void angles(const float *row, int rot, int lane, float sign, float *c, float *s) const {
-        const int e = (lane % LPR) * 8;
+    __device__ __forceinline__ void load(const float *row, int rot) {
         if (!turned) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) { c[i] = 1.f; s[i] = 0.f; }
+            for (int i = 0; i < 4; ++i) {
+                c[i] = f2(1.f, 1.f);
+                s[i] = f2(0.f, 0.f);
+            }
             return;
         }
+        const float4 *pc = reinterpret_cast<const float4 *>(row + (INTER ? A / 2 : A));
+        const float4 *qc = INTER ? reinterpret_cast<const float4 *>(row + B / 2) : pc + 1;
+        const float4 a = __ldg(pc), b = __ldg(qc), u = __ldg(pc + rot / 8), v = __ldg(qc + rot / 8);
+        c[0] = f2(a.x, a.y);
+        c[1] = f2(a.z, a.w);
+        c[2] = f2(b.x, b.y);
+        c[3] = f2(b.z, b.w);
+        s[0] = f2(u.x, u.y);
+        s[1] = f2(u.z, u.w);
+        s[2] = f2(v.x, v.y);
+        s[3] = f2(v.z, v.w);
+    }
+    // (xa, xb) turned by the angles, or (BACK) by their negatives, in place
+    template <bool BACK>
+    __device__ __forceinline__ void apply(uint64_t *xa, uint64_t *xb) const {
         if (INTER) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(row + e / 2));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(row + rot / 2 + e / 2));
-            const float ca[4] = {a.x, a.y, a.z, a.w}, sa[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[2 * i] = c[2 * i + 1] = ca[i];
-                s[2 * i] = -sign * sa[i];
-                s[2 * i + 1] = sign * sa[i];
+            for (int i = 0; i < 4; ++i) {  // pair i of each chunk: (a c - b s, b c + a s)
+                float c0, c1, s0, s1, p, q;
+                f2_split(c[i >> 1], c0, c1);
+                f2_split(s[i >> 1], s0, s1);
+                float ca = (i & 1) ? c1 : c0, sa = (i & 1) ? s1 : s0;
+                f2_split(c[2 + (i >> 1)], c0, c1);
+                f2_split(s[2 + (i >> 1)], s0, s1);
+                float cb = (i & 1) ? c1 : c0, sb = (i & 1) ? s1 : s0;
+                if (BACK) {
+                    sa = -sa;
+                    sb = -sb;
+                }
+                f2_split(xa[i], p, q);
+                xa[i] = f2(fmaf(p, ca, -(q * sa)), fmaf(q, ca, p * sa));
+                f2_split(xb[i], p, q);
+                xb[i] = f2(fmaf(p, cb, -(q * sb)), fmaf(q, cb, p * sb));
             }
         } else {
-            const int k = upper ? e - rot / 2 : e;
-            const float4 *pc = reinterpret_cast<const float4 *>(row + k);
-            const float4 *ps = reinterpret_cast<const float4 *>(row + rot / 2 + k);
-            const float4 a = __ldg(pc), b = __ldg(pc + 1), u = __ldg(ps), v = __ldg(ps + 1);
-            const float sg = upper ? sign : -sign;
-            c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w; c[4] = b.x; c[5] = b.y; c[6] = b.z; c[7] = b.w;
-            s[0] = sg * u.x; s[1] = sg * u.y; s[2] = sg * u.z; s[3] = sg * u.w;
-            s[4] = sg * v.x; s[5] = sg * v.y; s[6] = sg * v.z; s[7] = sg * v.w;
+            const uint64_t minus = f2(-1.f, -1.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t sn = fmul2(s[i], minus), a = xa[i];
+                xa[i] = ffma2(a, c[i], fmul2(xb[i], BACK ? s[i] : sn));
+                xb[i] = ffma2(xb[i], c[i], fmul2(a, BACK ? sn : s[i]));
+            }
         }
     }
 };
 
+// The backward holds more per value (weights, their gradients, angles), so there a lane takes one chunk of a
+// row, elements [e, e + 8), and the other halves of half pairs come from the lane `src`.
+template <int D, bool INTER>
+struct TurnBack {
+    static constexpr int LPR = D / 8;
+    int e, src;
+    bool turned, upper;
+    uint64_t c[4], s[4];  // g_i = c_i dy_i + s_i dy_p, p the other half of the pair
+    __device__ __forceinline__ TurnBack(int lane, int rot) {
+        const int l = lane % LPR, half = rot / 16;
+        e = l * 8;
+        turned = e < rot;
+        upper = !INTER && turned && l >= half;
+        src = (INTER || !turned) ? lane : (upper ? lane - half : lane + half);
+    }
+    __device__ __forceinline__ void load(const float *row, int rot) {
+        if (!turned) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = f2(1.f, 1.f);
+                s[i] = f2(0.f, 0.f);
+            }
+        } else if (INTER) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(row + e / 2));
+            const float4 b = __ldg(reinterpret_cast<const float4 *>(row + rot / 2 + e / 2));
+            c[0] = f2(a.x, a.x);
+            c[1] = f2(a.y, a.y);
+            c[2] = f2(a.z, a.z);
+            c[3] = f2(a.w, a.w);
+            s[0] = f2(b.x, -b.x);
+            s[1] = f2(b.y, -b.y);
+            s[2] = f2(b.z, -b.z);
+            s[3] = f2(b.w, -b.w);
+        } else {
+            const float4 *pc = reinterpret_cast<const float4 *>(row + (upper ? e - rot / 2 : e));
+            const float4 a = __ldg(pc), b = __ldg(pc + 1), u = __ldg(pc + rot / 8), v = __ldg(pc + rot / 8 + 1);
+            const uint64_t sg = upper ? f2(-1.f, -1.f) : f2(1.f, 1.f);
+            c[0] = f2(a.x, a.y);
+            c[1] = f2(a.z, a.w);
+            c[2] = f2(b.x, b.y);
+            c[3] = f2(b.z, b.w);
+            s[0] = fmul2(f2(u.x, u.y), sg);
+            s[1] = fmul2(f2(u.z, u.w), sg);
+            s[2] = fmul2(f2(v.x, v.y), sg);
+            s[3] = fmul2(f2(v.z, v.w), sg);
+        }
+    }
+};
+
+// Sums of two values over a row's lanes: the first exchange leaves each lane with one of the two, so the
+// pair costs log2(LPR) + 1 shuffles.
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ void row_sum2(float &a, float &b) {
+    const bool odd = threadIdx.x & 1;
+    float v = odd ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+#pragma unroll
+    for (int o = LPR / 2; o >= 2; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const float w = __shfl_xor_sync(0xffffffffu, v, 1);
+    a = odd ? w : v;
+    b = odd ? v : w;
+}
+
+// Sum over a row's lanes of both halves of two pair accumulators.
+template <int LPR>
+__device__ __forceinline__ float row_sum(uint64_t a, uint64_t b) {
+    float lo, hi;
+    f2_split(fadd2(a, b), lo, hi);
+    float v = lo + hi;
 #pragma unroll
     for (int o = LPR / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
@@ -150,15 +237,6 @@ __device__ __forceinline__ const float *angle_row(const QkNormParams &p, int64_t
     return p.cos_sin + pos * p.rot;
 }
 
-// Rows are read once: not kept in L1. (Not the read-only path: the output may be the input.)
-__device__ __forceinline__ uint4 ld_row(const uint16_t *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 // The kinds of rows (q, k, paged: v) have CTAs of their own: CTA blockIdx.x is number `cta` of `ctas` of
 // its kind.
 struct Share {
@@ -172,49 +250,83 @@ struct Share {
 };
 
 // A warp's walk over the work units of its kind: a unit is one token and up to p.heads_per_warp
-// consecutive heads, worked on in batches of BATCH heads. The next batch is asked for before the current
-// one is worked on, a unit's angles a batch before it begins, and its position a unit before that, so
-// that the loads that depend on one another are never waited for in a row.
+// consecutive heads, worked on in batches of `batch` heads.
 struct Walk {
-    int64_t unit, units, step, tok, ahead;  // ahead: position of the unit after the current one
-    int per_token, heads, hb, h1;
+    int64_t unit, units, step, tok;
+    int per_token, heads, per_unit, hb, h1;
     __device__ __forceinline__ Walk(const QkNormParams &p, const Share &sh) {
         per_token = sh.kind == 0 ? p.q_units : p.k_units;
         heads = sh.kind == 0 ? p.Hq : p.Hk;
+        per_unit = p.heads_per_warp;
         units = p.n * per_token;
         step = static_cast<int64_t>(sh.ctas) * kWarps;
         unit = static_cast<int64_t>(sh.cta) * kWarps + (threadIdx.x >> 5);
-        ahead = p.positions && unit < units ? p.positions[unit / per_token] : 0;
+        enter();
     }
-    // takes unit `unit`; its position
-    __device__ __forceinline__ int64_t enter(const QkNormParams &p) {
+    __device__ __forceinline__ bool more() const { return unit < units; }
+    __device__ __forceinline__ void enter() {
         tok = unit / per_token;
-        hb = static_cast<int>(unit - tok * per_token) * p.heads_per_warp;
-        h1 = min(heads, hb + p.heads_per_warp);
-        const int64_t pos = ahead;
-        if (p.positions && unit + step < units) ahead = p.positions[(unit + step) / per_token];
-        return pos;
+        hb = static_cast<int>(unit - tok * per_token) * per_unit;
+        h1 = min(heads, hb + per_unit);
     }
+    // to the next batch; true where it begins a unit
+    __device__ __forceinline__ bool next(int batch) {
+        hb += batch;
+        if (hb < h1) return false;
+        unit += step;
+        enter();
+        return true;
+    }
+    // token of the unit after this one (this one's where there is none)
+    __device__ __forceinline__ int64_t next_token() const { return unit + step < units ? (unit + step) / per_token : tok; }
 };
 
-constexpr int kFwdRows = 4, kBwdRows = 2;  // rows a lane takes at a time
+// Measured at 8192 tokens of 64 heads of 128 (forward / backward, us): two rows a lane, two CTAs an SM and
+// four slots 50.6 / 77.5 (as fast as a plain copy of the forward's bytes, 51); three CTAs, whose registers
+// spill, 54.5 / 105; one row and six slots 50.3 / 98; six slots 50.8 / 79; the next rows in registers
+// instead of a ring 60.5 / 86.
+constexpr int kRows = 2;   // rows a lane takes at a time
+constexpr int kPerSm = 2;  // CTAs an SM
+constexpr int kSlots = 4;  // batches in the ring, one of them being worked on
+
+// Rows on their way: each thread copies its own chunks into its own places of a ring of kSlots batches in
+// shared memory (cp.async) and reads them back itself, so nothing has to be synchronised, and what is in
+// flight does not take registers. V: 16-byte chunks a thread takes of a batch.
+template <int V>
+struct Ring {
+    static constexpr int BYTES = kSlots * V * kThreads * 16;
+    uint32_t base;
+    int in, out;
+    __device__ __forceinline__ explicit Ring(const uint8_t *smem) : base(smem_u32(smem) + threadIdx.x * 16), in(0), out(0) {}
+    __device__ __forceinline__ void put(int v, const uint16_t *src, bool there) const {
+        cp_async_16_zfill(base + (in * V + v) * kThreads * 16, src, there ? 16u : 0u);
+    }
+    __device__ __forceinline__ void filled() {  // (also where nothing was put: batches are counted)
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in = in + 1 == kSlots ? 0 : in + 1;
+    }
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory"); }
+    __device__ __forceinline__ uint4 get(int v) const { return ld_shared_v4(base + (out * V + v) * kThreads * 16); }
+    __device__ __forceinline__ void next() { out = out + 1 == kSlots ? 0 : out + 1; }
+};
 
 // PAGED: k and v rows go to the token's slot in the pages.
 template <int D, bool BF16, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_fwd_kernel(const QkNormParams p) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, U = kFwdRows, BATCH = RPI * U;  // lanes a row, rows of a load
-    const int lane = threadIdx.x & 31, sub = lane % LPR, row_in = lane / LPR;
+__global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_fwd_kernel(const QkNormParams p) {
+    constexpr int LPR = D / 16, RPI = 32 / LPR, U = kRows, BATCH = RPI * U;  // lanes a row, rows of a load
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 31, row_in = lane / LPR;
     const Share sh(p);
     const int kind = sh.kind;
-    const uint16_t *x0 = static_cast<const uint16_t *>(kind == 0 ? p.q : (kind == 1 ? p.k : p.v)) + sub * 8;
+    const uint16_t *x0 = static_cast<const uint16_t *>(kind == 0 ? p.q : (kind == 1 ? p.k : p.v));
     const int64_t xs = kind == 0 ? p.q_stride : (kind == 1 ? p.k_stride : p.v_stride);
     bool bad = false, lost = false;
     Walk w(p, sh);
+    if (!w.more()) return;
     // where token w.tok's row of heads goes (PAGED: null where it has no place), and its position
     auto place = [&](int64_t &pos) -> uint16_t * {
         if constexpr (!PAGED) {
-            return static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) +
-                   w.tok * (kind == 0 ? p.q_out_stride : p.k_out_stride) + sub * 8;
+            return static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) + w.tok * (kind == 0 ? p.q_out_stride : p.k_out_stride);
         } else {
             // rows of no sequence stay as they are
             if (w.tok < p.cu_seqlens[0] || w.tok >= p.cu_seqlens[p.num_seqs]) return nullptr;
@@ -222,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_fwd_kernel(const QkNormPa
             if (b < 0 || b >= p.num_seqs) return nullptr;  // offsets that do not rise
             const int64_t slot = static_cast<int64_t>(p.kv_lens[b]) - p.cu_seqlens[b + 1] + w.tok;
             if (!p.positions) pos = slot;
-            if (kind == 0) return static_cast<uint16_t *>(p.q_out) + w.tok * p.q_out_stride + sub * 8;
+            if (kind == 0) return static_cast<uint16_t *>(p.q_out) + w.tok * p.q_out_stride;
             int pg = -1;
             if (slot >= 0 && slot < (static_cast<int64_t>(p.max_blocks) << p.page_shift))
                 pg = p.block_table[static_cast<int64_t>(b) * p.max_blocks + (slot >> p.page_shift)];
@@ -231,196 +343,207 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_fwd_kernel(const QkNormPa
                 return nullptr;
             }
             const int64_t row = (static_cast<int64_t>(pg) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
-            return static_cast<uint16_t *>(kind == 1 ? p.k_out : p.v_out) + row * p.Hk * D + sub * 8;
+            return static_cast<uint16_t *>(kind == 1 ? p.k_out : p.v_out) + row * p.Hk * D;
         }
     };
-    auto load = [&](uint4 *v) {
+    Turn<D, INTER> turn(lane, p.rot);
+    Ring<2 * U> ring(smem);
+    Walk wl = w;  // of the loads
+    auto fetch = [&]() {
+        if (wl.more()) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int h = wl.hb + i * RPI + row_in;
+                const bool there = h < wl.h1;
+                const uint16_t *x = x0 + wl.tok * xs + (there ? h * D : 0);
+                ring.put(2 * i, x + turn.A, there);
+                ring.put(2 * i + 1, x + turn.B, there);
+            }
+            wl.next(BATCH);
+        }
+        ring.filled();
+    };
+#pragma unroll
+    for (int k = 0; k < kSlots - 1; ++k) fetch();
+    uint64_t wa[4], wb[4];
+    if (kind < 2) {
+        load_weights<BF16>(kind == 0 ? p.wq : p.wk, p.w32, turn.A, wa);
+        load_weights<BF16>(kind == 0 ? p.wq : p.wk, p.w32, turn.B, wb);
+    }
+    int64_t pos = p.positions && kind < 2 ? p.positions[w.tok] : 0;
+    uint16_t *dst = place(pos);
+    if (kind < 2) turn.load(angle_row(p, pos, bad), p.rot);
+    int64_t pos_next = p.positions && kind < 2 ? p.positions[w.next_token()] : 0;
+    while (true) {
+        ring.wait();
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int h = w.hb + i * RPI + row_in;
-            v[i] = h < w.h1 ? ld_row(x0 + w.tok * xs + h * D) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    const Turn<D, INTER> turn(lane, p.rot);
-    const void *wt = kind == 0 ? p.wq : p.wk;
-    float wi[8], wp[8];
-    if (kind < 2) {
-        load_weights<BF16>(wt, p.w32, sub * 8, wi);
-        load_weights<BF16>(wt, p.w32, turn.pe, wp);
-    }
-    uint4 v[U];
-    float c[8], s[8], a[8], b[8];  // angles of the unit to come; y_i = r (x_i a_i + x_p b_i)
-    bool more = w.unit < w.units, fresh = true;
-    uint16_t *y = nullptr;
-    if (more) {
-        int64_t pos = w.enter(p);
-        load(v);
-        y = place(pos);
-        if (kind < 2) turn.angles(angle_row(p, pos, bad), p.rot, lane, 1.f, c, s);
-    }
-#pragma unroll 1
-    while (more) {
-        if (fresh && kind < 2) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                a[i] = wi[i] * c[i];
-                b[i] = wp[INTER ? (i ^ 1) : i] * s[i];
-            }
-        }
-        const int hb = w.hb, h1 = w.h1;
-        uint16_t *const dst = y;
-        uint4 nv[U];
-        w.hb += BATCH;
-        fresh = w.hb >= w.h1;
-        if (fresh) {
-            w.unit += w.step;
-            more = w.unit < w.units;
-            if (more) {
-                int64_t pos = w.enter(p);
-                load(nv);
-                y = place(pos);
-                if (kind < 2) turn.angles(angle_row(p, pos, bad), p.rot, lane, 1.f, c, s);
-            }
-        } else {
-            load(nv);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = hb + i * RPI + row_in;
+            uint16_t *out = dst + h * D;
+            const bool store = dst && h < w.h1;
+            const uint4 va = ring.get(2 * i), vb = ring.get(2 * i + 1);
             if (PAGED && kind == 2) {  // values: a copy
-                if (dst && h < h1) *reinterpret_cast<uint4 *>(dst + h * D) = v[i];
+                if (store) {
+                    *reinterpret_cast<uint4 *>(out + turn.A) = va;
+                    *reinterpret_cast<uint4 *>(out + turn.B) = vb;
+                }
                 continue;
             }
-            float xi[8], xp[8], out[8];
-            unpack8<BF16>(v[i], xi);
-            if (INTER) {
+            uint64_t xa[4], xb[4], ssa = f2(0.f, 0.f), ssb = ssa;
+            unpack8<BF16>(va, xa);
+            unpack8<BF16>(vb, xb);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) xp[k] = xi[k ^ 1];
-            } else {
-                unpack8<BF16>(shfl4(v[i], turn.src), xp);
+            for (int k = 0; k < 4; ++k) {
+                ssa = ffma2(xa[k], xa[k], ssa);
+                ssb = ffma2(xb[k], xb[k], ssb);
+                xa[k] = fmul2(xa[k], wa[k]);
+                xb[k] = fmul2(xb[k], wb[k]);
             }
-            float ss = 0.f;
+            const float r = rsqrtf(row_sum<LPR>(ssa, ssb) * (1.0f / D) + p.eps);
+            const uint64_t r2 = f2(r, r);
+            turn.template apply<false>(xa, xb);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(xi[k], xi[k], ss);
-            const float r = rsqrtf(row_sum<LPR>(ss) * (1.0f / D) + p.eps);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) out[k] = r * fmaf(xi[k], a[k], xp[k] * b[k]);
-            if (dst && h < h1) *reinterpret_cast<uint4 *>(dst + h * D) = pack8<BF16>(out);
+            for (int k = 0; k < 4; ++k) {
+                xa[k] = fmul2(xa[k], r2);
+                xb[k] = fmul2(xb[k], r2);
+            }
+            if (store) {
+                *reinterpret_cast<uint4 *>(out + turn.A) = pack8<BF16>(xa);
+                *reinterpret_cast<uint4 *>(out + turn.B) = pack8<BF16>(xb);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < U; ++i) v[i] = nv[i];
+        ring.next();
+        fetch();  // into the slot of the batch before
+        if (w.next(BATCH)) {
+            if (!w.more()) break;
+            pos = pos_next;
+            dst = place(pos);
+            if (kind < 2) {
+                turn.load(angle_row(p, pos, bad), p.rot);
+                if (p.positions) pos_next = p.positions[w.next_token()];
+            }
+        }
     }
+    cp_async_wait_all();
     if (bad && lane == 0) record_error(FA_ERR_INDEX, 700);
     if (lost && lane == 0) record_error(FA_ERR_INDEX, 701);
 }
 
 // Backward: the same walk over x and dy, adding g x r of each row to eight weight-gradient sums a lane.
 template <int D, bool BF16, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const QkNormParams p) {
-    constexpr int LPR = D / 8, RPI = 32 / LPR, U = kBwdRows, BATCH = RPI * U;
+__global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_bwd_kernel(const QkNormParams p) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, U = kRows, BATCH = RPI * U;
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float part[kWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR, row_in = lane / LPR;
-    const Turn<D, INTER> turn(lane, p.rot);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row_in = lane / LPR;
     const Share sh(p);
     const int kind = sh.kind;
-    const uint16_t *x0 = static_cast<const uint16_t *>(kind == 0 ? p.q : p.k) + sub * 8;
-    const uint16_t *dy0 = static_cast<const uint16_t *>(kind == 0 ? p.dq_out : p.dk_out) + sub * 8;
-    uint16_t *dx0 = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) + sub * 8;
+    TurnBack<D, INTER> turn(lane, p.rot);
+    const uint16_t *x0 = static_cast<const uint16_t *>(kind == 0 ? p.q : p.k) + turn.e;
+    const uint16_t *dy0 = static_cast<const uint16_t *>(kind == 0 ? p.dq_out : p.dk_out) + turn.e;
+    uint16_t *dx0 = static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) + turn.e;
     const int64_t xs = kind == 0 ? p.q_stride : p.k_stride, dys = kind == 0 ? p.dq_out_stride : p.dk_out_stride;
     const int64_t dxs = kind == 0 ? p.q_out_stride : p.k_out_stride;
     bool bad = false;
-    Walk w(p, sh);
-    float wi[8], dw[8];
-    load_weights<BF16>(kind == 0 ? p.wq : p.wk, p.w32, sub * 8, wi);
+    Walk w(p, sh), wl = w;  // wl: of the loads
+    Ring<2 * U> ring(smem);
+    auto fetch = [&]() {
+        if (wl.more()) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[k] = 0.f;
-    auto load = [&](uint4 *ox, uint4 *oy) {
+            for (int i = 0; i < U; ++i) {
+                const int h = wl.hb + i * RPI + row_in;
+                const bool there = h < wl.h1;
+                const int at = there ? h * D : 0;
+                ring.put(2 * i, x0 + wl.tok * xs + at, there);
+                ring.put(2 * i + 1, dy0 + wl.tok * dys + at, there);
+            }
+            wl.next(BATCH);
+        }
+        ring.filled();
+    };
+#pragma unroll
+    for (int k = 0; k < kSlots - 1; ++k) fetch();
+    uint64_t wt[4], dw[4];
+    load_weights<BF16>(kind == 0 ? p.wq : p.wk, p.w32, turn.e, wt);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dw[k] = f2(0.f, 0.f);
+    int64_t pos_next = 0;
+    if (w.more()) {
+        turn.load(angle_row(p, p.positions[w.tok], bad), p.rot);
+        pos_next = p.positions[w.next_token()];
+    }
+    while (w.more()) {
+        ring.wait();
+        uint16_t *const dst = dx0 + w.tok * dxs;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int h = w.hb + i * RPI + row_in;
-            ox[i] = h < w.h1 ? ld_row(x0 + w.tok * xs + h * D) : make_uint4(0, 0, 0, 0);
-            oy[i] = h < w.h1 ? ld_row(dy0 + w.tok * dys + h * D) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    uint4 vx[U], vy[U];
-    float c[8], s[8], nc[8], ns[8];
-    bool more = w.unit < w.units, fresh = true;
-    if (more) {
-        const int64_t pos = w.enter(p);
-        load(vx, vy);
-        turn.angles(angle_row(p, pos, bad), p.rot, lane, -1.f, nc, ns);
-    }
-#pragma unroll 1
-    while (more) {
-        if (fresh) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i] = nc[i];
-                s[i] = ns[i];
-            }
-        }
-        const int hb = w.hb, h1 = w.h1;
-        uint16_t *const dx = dx0 + w.tok * dxs;
-        uint4 nx[U], ny[U];
-        w.hb += BATCH;
-        fresh = w.hb >= w.h1;
-        if (fresh) {
-            w.unit += w.step;
-            more = w.unit < w.units;
-            if (more) {
-                const int64_t pos = w.enter(p);
-                load(nx, ny);
-                turn.angles(angle_row(p, pos, bad), p.rot, lane, -1.f, nc, ns);
-            }
-        } else {
-            load(nx, ny);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = hb + i * RPI + row_in;
-            float xi[8], yi[8], yp[8], u[8];
-            unpack8<BF16>(vx[i], xi);
-            unpack8<BF16>(vy[i], yi);
+            const bool there = h < w.h1;
+            const uint4 vx = ring.get(2 * i), vy = ring.get(2 * i + 1);
+            uint64_t x[4], g[4], o[4];
+            unpack8<BF16>(vx, x);
+            unpack8<BF16>(vy, g);
             if (INTER) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) yp[k] = yi[k ^ 1];
+                for (int k = 0; k < 4; ++k) {
+                    float lo, hi;
+                    f2_split(g[k], lo, hi);
+                    o[k] = f2(hi, lo);
+                }
             } else {
-                unpack8<BF16>(shfl4(vy[i], turn.src), yp);
+                uint4 other;
+                other.x = __shfl_sync(0xffffffffu, vy.x, turn.src);
+                other.y = __shfl_sync(0xffffffffu, vy.y, turn.src);
+                other.z = __shfl_sync(0xffffffffu, vy.z, turn.src);
+                other.w = __shfl_sync(0xffffffffu, vy.w, turn.src);
+                unpack8<BF16>(other, o);
             }
-            float ss = 0.f, t = 0.f;
+            uint64_t ss2 = f2(0.f, 0.f), t2 = ss2;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                u[k] = fmaf(yi[k], c[k], yp[k] * s[k]);  // g = R^T dy
-                ss = fmaf(xi[k], xi[k], ss);
-                t = fmaf(u[k] * wi[k], xi[k], t);
+            for (int k = 0; k < 4; ++k) {
+                g[k] = ffma2(g[k], turn.c[k], fmul2(o[k], turn.s[k]));  // g = R^T dy
+                o[k] = fmul2(g[k], wt[k]);                              // u
+                ss2 = ffma2(x[k], x[k], ss2);
+                t2 = ffma2(o[k], x[k], t2);
             }
-            ss = row_sum<LPR>(ss);
-            t = row_sum<LPR>(t);
+            float ss, t, hi;
+            f2_split(ss2, ss, hi);
+            ss += hi;
+            f2_split(t2, t, hi);
+            t += hi;
+            row_sum2<LPR>(ss, t);
             const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-            const float q = r * r * t * (1.0f / D);
+            const float q = -r * r * t * (1.0f / D);
+            const uint64_t r2 = f2(r, r), q2 = f2(q, q), rw = there ? r2 : f2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (h < h1) dw[k] = fmaf(u[k], xi[k] * r, dw[k]);
-                u[k] = r * (u[k] * wi[k] - xi[k] * q);
+            for (int k = 0; k < 4; ++k) {
+                dw[k] = ffma2(g[k], fmul2(x[k], rw), dw[k]);
+                o[k] = fmul2(ffma2(x[k], q2, o[k]), r2);  // r (u - x r^2 t / D)
             }
-            if (h < h1) *reinterpret_cast<uint4 *>(dx + h * D) = pack8<BF16>(u);
+            if (there) *reinterpret_cast<uint4 *>(dst + h * D) = pack8<BF16>(o);
         }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            vx[i] = nx[i];
-            vy[i] = ny[i];
+        ring.next();
+        fetch();  // into the slot of the batch before
+        if (w.next(BATCH) && w.more()) {
+            turn.load(angle_row(p, pos_next, bad), p.rot);
+            pos_next = p.positions[w.next_token()];
         }
     }
+    cp_async_wait_all();
     if (bad && lane == 0) record_error(FA_ERR_INDEX, 700);
     if (!p.partials) return;
     // the rows of a warp, then the CTA's warps, in a fixed order
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < 4; ++k) {
+        float x[2];
+        f2_split(dw[k], x[0], x[1]);
 #pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
-    if (row_in == 0)
+        for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) part[warp][sub * 8 + k] = dw[k];
+            for (int o = LPR; o < 32; o <<= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+            if (row_in == 0) part[warp][turn.e + 2 * k + i] = x[i];
+        }
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < D; e += kThreads) {
         float sum = 0.f;
@@ -451,12 +574,29 @@ __global__ void __launch_bounds__(1024) qk_norm_dw_kernel(const QkNormParams p, 
     }
 }
 
+// Launches a kernel with the ring's dynamic shared memory (the opt-in above 48 KB is a per-device function
+// attribute, set at the kernel's first launch on a device; setting it twice is harmless).
+template <auto Kernel>
+cudaError_t launch_ring(int bytes, int grid, const QkNormParams &p, cudaStream_t st) {
+    static uint64_t attr_set_mask = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(__atomic_load_n(&attr_set_mask, __ATOMIC_ACQUIRE) & bit)) {
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        __atomic_fetch_or(&attr_set_mask, bit, __ATOMIC_RELEASE);
+    }
+    Kernel<<<grid, kThreads, bytes, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <int D, bool BF16, bool INTER>
 cudaError_t launch_d(bool backward, QkNormParams p, cudaStream_t st) {
-    constexpr int RPI = 32 / (D / 8);
-    const int batch = RPI * (backward ? kBwdRows : kFwdRows);  // heads a warp works on at a time
+    const int batch = backward ? 32 / (D / 8) * kRows : 32 / (D / 16) * kRows;  // heads a warp works on at a time
     const bool paged = p.cu_seqlens != nullptr;
-    // Two CTAs an SM, shared out by the kinds' heads. A unit is one batch while that leaves CTAs idle, else
+    // kPerSm CTAs an SM, shared out by the kinds' heads. A unit is one batch while that leaves CTAs idle, else
     // up to four batches of a token, which share its angles.
     const int most = kQkNormCtas;
     auto units = [&](int heads, int per) { return static_cast<int64_t>((heads + per - 1) / per); };
@@ -476,8 +616,7 @@ cudaError_t launch_d(bool backward, QkNormParams p, cudaStream_t st) {
     p.ctas_k = share(p.Hk, p.k_units);
     const int grid = p.ctas_q + p.ctas_k + (paged ? p.ctas_k : 0);
     if (backward) {
-        qk_norm_bwd_kernel<D, BF16, INTER><<<grid, kThreads, 0, st>>>(p);
-        cudaError_t e = cudaGetLastError();
+        cudaError_t e = launch_ring<qk_norm_bwd_kernel<D, BF16, INTER>>(Ring<2 * kRows>::BYTES, grid, p, st);
         if (e != cudaSuccess || !p.partials) return e;
         cudaLaunchConfig_t cfg = {};  // waits on the device for the kernel above
         cfg.gridDim = dim3(D / 32, 2, 1);
@@ -491,11 +630,9 @@ cudaError_t launch_d(bool backward, QkNormParams p, cudaStream_t st) {
         e = cudaLaunchKernelEx(&cfg, qk_norm_dw_kernel, p, D);
         return e != cudaSuccess ? e : cudaGetLastError();
     }
-    if (paged)
-        qk_norm_fwd_kernel<D, BF16, INTER, true><<<grid, kThreads, 0, st>>>(p);
-    else
-        qk_norm_fwd_kernel<D, BF16, INTER, false><<<grid, kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    constexpr int bytes = Ring<2 * kRows>::BYTES;
+    return paged ? launch_ring<qk_norm_fwd_kernel<D, BF16, INTER, true>>(bytes, grid, p, st)
+                 : launch_ring<qk_norm_fwd_kernel<D, BF16, INTER, false>>(bytes, grid, p, st);
 }
 
 template <int D>
