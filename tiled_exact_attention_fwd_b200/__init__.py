@@ -1,7 +1,7 @@
 """Python binding of libfa (include/fa.h): exact attention forward on B200 (sm_100a).
 
-This module only marshals torch CUDA tensors into the C ABI: every step of the
-computation runs in the library's kernels. There is no fallback: if libfa.so is not
+This module and its compiled part (csrc/fa_torch.cpp) only marshal torch CUDA tensors into the C
+ABI: every step of the computation runs in the library's kernels. There is no fallback: if libfa.so is not
 built, every call raises.
 
     out, lse = fa_fwd(q, k, v, causal=True)                         # dense (B, S, H, D)
@@ -427,112 +427,33 @@ def fa_pad(x: torch.Tensor, indices: torch.Tensor, batch: int, total_len: int,
     return out
 
 
-# The calls around a paged cache run once or more per generated token, so what they do on the host counts:
-# checks compare plain values, and the current device and stream are asked for directly.
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_ext = None
 
 
-def _elsewhere(t: torch.Tensor, stream) -> bool:
-    """Whether a call has to change the current device or stream first."""
-    return stream is not None or (t.is_cuda and t.get_device() != _current_device())
+def _binding():
+    """The compiled marshalling of the calls below (raises if it has not been built). They run once or more
+    per generated token, and what they would do in Python took longer than their kernels."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _fa_torch
+        except ImportError as e:
+            raise RuntimeError("_fa_torch.so is not built; run `python -m tiled_exact_attention_fwd_b200.build`") from e
+        _ext = _fa_torch
+    return _ext
 
 
 def _on_stream(t: torch.Tensor, stream):
-    """The operands' device and, where one is given, `stream` made current, so that what the call
-    allocates (results, workspace) belongs to the stream that uses it."""
+    """`stream` made current (and its device), so that what the call allocates (results, workspace)
+    belongs to the stream that uses it."""
     if not t.is_cuda:
         raise ValueError("the operands must be CUDA tensors")
-    if stream is None:
-        return torch.cuda.device(t.device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     if stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     return torch.cuda.stream(stream)
-
-
-def _heads(name: str, t: torch.Tensor) -> Tuple[int, int]:
-    """(token rows, elements from one to the next) of a (..., H, D) tensor whose heads are contiguous
-    in a token and whose tokens lie at one stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    shape = t.shape
-    if len(shape) < 3:
-        raise ValueError(f"{name} must be (..., heads, head dim)")
-    H, D = shape[-2], shape[-1]
-    st = t.stride()
-    if (D > 1 and st[-1] != 1) or (H > 1 and st[-2] != D):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    if len(shape) == 3:
-        n = shape[0]
-        return n, (st[0] if n > 1 else H * D)
-    n, stride = 1, H * D
-    for size, step in zip(reversed(shape[:-2]), reversed(st[:-2])):
-        if size == 1:
-            continue
-        if n == 1:
-            stride = step
-        elif step != stride * n:
-            raise ValueError(f"the tokens of {name} must lie at one stride")
-        n *= size
-    return (n if t.numel() else 0), stride
-
-
-def _out_heads(name: str, t: torch.Tensor, like: torch.Tensor) -> int:
-    """The token stride of a caller-given tensor of like's shape, dtype and device."""
-    if t.shape != like.shape or t.dtype != like.dtype or t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be {like.dtype} {tuple(like.shape)} on {like.device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return _heads(name, t)[1]
-
-
-def _plain(name: str, t: torch.Tensor, dtype, dev: int) -> None:
-    """A contiguous tensor of one dtype on device `dev`."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
-
-
-def _norm_args(q, k, q_weight, k_weight, cos_sin, positions):
-    """Checks of what the norm entry points share -> (n, q stride, k stride, dtype code, the C call's
-    weights and angles)."""
-    n, qs = _heads("q", q)
-    _, ks = _heads("k", k)
-    shape, dt, dev = q.shape, q.dtype, q.get_device()
-    code = _dtype_code(q)
-    if k.shape[:-2] != shape[:-2] or k.shape[-1] != shape[-1] or k.dtype != dt or k.get_device() != dev:
-        raise ValueError("q and k must share their leading shape, head dim, dtype and device")
-    w32, wq, wk = False, None, None
-    if q_weight is not None:
-        w32 = q_weight.dtype == torch.float32
-        _plain("q_weight", q_weight, torch.float32 if w32 else dt, dev)
-        wq = q_weight.data_ptr()
-    if k_weight is not None:
-        k32 = k_weight.dtype == torch.float32
-        if q_weight is not None and k32 != w32:
-            raise ValueError("q_weight and k_weight must share one dtype")
-        w32 = k32
-        _plain("k_weight", k_weight, torch.float32 if w32 else dt, dev)
-        wk = k_weight.data_ptr()
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dim() != 1 or w.shape[0] != shape[-1]):
-            raise ValueError(f"the weights must be ({shape[-1]},), got {tuple(w.shape)}")
-    _plain("cos_sin", cos_sin, torch.float32, dev)
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be (positions, rot_dim)")
-    if positions is None:
-        pos = None
-    else:
-        _plain("positions", positions, torch.int64, dev)
-        if positions.shape != shape[:-2]:
-            raise ValueError("positions must be of q's leading shape")
-        pos = positions.data_ptr()
-    rows, rot = cos_sin.shape
-    return n, qs, ks, code, (wq, wk, w32, cos_sin.data_ptr(), rows, rot, pos)
 
 
 def fa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.Tensor], k_weight: Optional[torch.Tensor],
@@ -542,23 +463,12 @@ def fa_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[torch.T
     """RMS norm of q (..., Hq, D) and k (..., Hkv, D) for each head, weights (D,) or None, then the
     rotation by cos_sin[positions] (float32 (positions, rot_dim): cosines, then sines). q and k may be
     views of a fused projection. q_out and k_out may be q and k themselves."""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _on_stream(q, stream):
             return fa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, q_out, k_out)
-    n, qs, ks, code, args = _norm_args(q, k, q_weight, k_weight, cos_sin, positions)
     if positions is None:
         raise ValueError("positions must be given")
-    Hq, Hkv, D = q.shape[-2], k.shape[-2], q.shape[-1]
-    if q_out is None:
-        q_out, qos = q.new_empty(q.shape), Hq * D
-    else:
-        qos = _out_heads("q_out", q_out, q)
-    if k_out is None:
-        k_out, kos = k.new_empty(k.shape), Hkv * D
-    else:
-        kos = _out_heads("k_out", k_out, k)
-    st = lib().fa_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, *args, q_out.data_ptr(), qos, k_out.data_ptr(), kos, n, Hq,
-                               Hkv, D, eps, interleaved, code, _current_raw_stream(q.get_device()))
+    st, q_out, k_out = _binding().qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, q_out, k_out)
     if st:
         raise FAError(st, "fa_qk_norm_rope")
     return q_out, k_out
@@ -570,57 +480,15 @@ def fa_qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, q_weight: Optional[tor
                         stream=None):
     """Gradients of fa_qk_norm_rope: (dq, dk, dq_weight, dk_weight), the weights' in float32 (None where
     the weight is None)."""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _on_stream(q, stream):
             return fa_qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, eps, interleaved)
-    n, qs, ks, code, args = _norm_args(q, k, q_weight, k_weight, cos_sin, positions)
     if positions is None:
         raise ValueError("positions must be given")
-    dqs, dks = _out_heads("dq_out", dq_out, q), _out_heads("dk_out", dk_out, k)
-    Hq, Hkv, D = q.shape[-2], k.shape[-2], q.shape[-1]
-    dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
-    dwq = None if q_weight is None else torch.empty(D, dtype=torch.float32, device=q.device)
-    dwk = None if k_weight is None else torch.empty(D, dtype=torch.float32, device=q.device)
-    L, ws, size = lib(), None, 0
-    if dwq is not None or dwk is not None:
-        size = L.fa_qk_norm_rope_bwd_workspace(D)
-        ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-    st = L.fa_qk_norm_rope_bwd(q.data_ptr(), qs, k.data_ptr(), ks, *args, dq_out.data_ptr(), dqs, dk_out.data_ptr(), dks,
-                               dq.data_ptr(), Hq * D, dk.data_ptr(), Hkv * D, _ptr(dwq), _ptr(dwk), _ptr(ws), size, n, Hq,
-                               Hkv, D, eps, interleaved, code, _current_raw_stream(q.get_device()))
+    st, *grads = _binding().qk_norm_rope_bwd(q, k, q_weight, k_weight, cos_sin, positions, dq_out, dk_out, eps, interleaved)
     if st:
         raise FAError(st, "fa_qk_norm_rope_bwd")
-    return dq, dk, dwq, dwk
-
-
-def _paged_args(k_cache, v_cache, block_table, kv_lens):
-    """Checks of page pools and their table -> (device, sequences, the C call's table arguments)."""
-    if not k_cache.is_cuda or not k_cache.is_contiguous():
-        raise ValueError("k_cache must be a contiguous CUDA tensor")
-    dev = k_cache.get_device()
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError("k_cache must be (num_pages, page_size, Hkv, D)")
-    if v_cache is not None:
-        _plain("v_cache", v_cache, k_cache.dtype, dev)
-        if v_cache.shape != shape:
-            raise ValueError("k_cache and v_cache must share one shape")
-    _plain("kv_lens", kv_lens, torch.int32, dev)
-    _plain("block_table", block_table, torch.int32, dev)
-    ts = block_table.shape
-    num = kv_lens.numel()
-    if kv_lens.dim() != 1 or len(ts) != 2 or ts[0] != num:
-        raise ValueError("kv_lens must be (sequences,) and block_table (sequences, max_blocks_per_seq)")
-    return dev, num, (block_table.data_ptr(), ts[1], shape[1], shape[0])
-
-
-def _packed_args(q, k_cache, cu_seqlens, num, dev):
-    """Checks of packed new tokens over pools: q (total, Hq, D), cu_seqlens (sequences + 1)."""
-    _plain("cu_seqlens", cu_seqlens, torch.int32, dev)
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != num + 1:
-        raise ValueError("cu_seqlens must hold one more entry than kv_lens")
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or q.dtype != k_cache.dtype or q.get_device() != dev:
-        raise ValueError("q must be (total, Hq, D) with the caches' head dim, dtype and device")
+    return tuple(grads)
 
 
 def fa_qk_norm_rope_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -631,24 +499,12 @@ def fa_qk_norm_rope_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_w
     """fa_qk_norm_rope of packed new tokens q (total, Hq, D), k and v (total, Hkv, D), with k and v
     written into the pages: new token i of sequence b's n goes to slot kv_lens[b] - n + i (kv_lens
     counts the new tokens). positions None: the slot. Returns q_out."""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _on_stream(q, stream):
             return fa_qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, block_table,
                                          cu_seqlens, kv_lens, eps, interleaved, q_out)
-    n, qs, ks, code, args = _norm_args(q, k, q_weight, k_weight, cos_sin, positions)
-    dev, num, table = _paged_args(k_cache, v_cache, block_table, kv_lens)
-    _packed_args(q, k_cache, cu_seqlens, num, dev)
-    if k.shape[1] != k_cache.shape[2]:
-        raise ValueError("k and v must be (total, Hkv, D) like the caches' rows")
-    vs = _out_heads("v", v, k)
-    _, Hq, D = q.shape
-    if q_out is None:
-        q_out, qos = q.new_empty(q.shape), Hq * D
-    else:
-        qos = _out_heads("q_out", q_out, q)
-    st = lib().fa_qk_norm_rope_paged(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, *args, q_out.data_ptr(), qos,
-                                     k_cache.data_ptr(), v_cache.data_ptr(), *table, cu_seqlens.data_ptr(), kv_lens.data_ptr(),
-                                     num, n, Hq, k.shape[1], D, eps, interleaved, code, _current_raw_stream(dev))
+    st, q_out = _binding().qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos_sin, positions, k_cache, v_cache, block_table,
+                                              cu_seqlens, kv_lens, eps, interleaved, q_out)
     if st:
         raise FAError(st, "fa_qk_norm_rope_paged")
     return q_out
@@ -663,35 +519,12 @@ def fa_fwd_paged_chunk(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     (num_pages, page_size, Hkv, D), int32 block_table (B, max_blocks_per_seq), cu_seqlens (B + 1) and
     kv_lens (B), which counts the new tokens -> out (total, Hq, D), lse (Hq, total) fp32. `workspace`
     (uint8, of fa_fwd_paged_chunk_workspace(...) bytes) is allocated by the call unless given."""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _on_stream(q, stream):
             return fa_fwd_paged_chunk(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, max_q_len, out, lse, scale,
                                       causal, return_lse, workspace)
-    dev, num, table = _paged_args(k_cache, v_cache, block_table, kv_lens)
-    _packed_args(q, k_cache, cu_seqlens, num, dev)
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    total, Hq, D = q.shape
-    Hkv = k_cache.shape[2]
-    code, L = _dtype_code(q), lib()
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _like("out", out, q.shape, q.dtype)
-    if lse is not None:
-        _like("lse", lse, (Hq, total), torch.float32)
-    elif return_lse:
-        lse = torch.empty((Hq, total), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        size = L.fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    else:
-        _cuda_contig("workspace", workspace)
-        size = workspace.numel() * workspace.element_size()
-    _same_device(q, out, lse, workspace)
-    st = L.fa_fwd_paged_chunk(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), *table, cu_seqlens.data_ptr(),
-                              kv_lens.data_ptr(), num, total, max_q_len, out.data_ptr(), _ptr(lse), workspace.data_ptr(), size,
-                              Hq, Hkv, D, scale if scale else 0.0, causal, code, _current_raw_stream(dev))
+    st, out, lse = _binding().fwd_paged_chunk(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, int(max_q_len), out, lse,
+                                              float(scale) if scale else 0.0, bool(causal), bool(return_lse), workspace)
     if st:
         raise FAError(st, "fa_fwd_paged_chunk")
     return out, lse
@@ -702,17 +535,6 @@ def fa_fwd_paged_chunk_workspace(Hq: int, Hkv: int, D: int, max_q_len: int) -> i
     return lib().fa_fwd_paged_chunk_workspace(int(Hq), int(Hkv), int(D), int(max_q_len))
 
 
-def fa_paged_key_weights_workspace(Hq: int, Hkv: int, D: int, max_q_len: int) -> int:
-    """Bytes of fa_paged_key_weights's workspace (0: none)."""
-    return lib().fa_paged_key_weights_workspace(int(Hq), int(Hkv), int(D), int(max_q_len))
-
-
-def _key_weights_args(weights, num, Hkv, dev):
-    _plain("weights", weights, torch.float32, dev)
-    if weights.dim() != 3 or weights.shape[0] != num or weights.shape[1] != Hkv:
-        raise ValueError("weights must be (sequences, Hkv, width)")
-
-
 def fa_paged_key_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
                          kv_lens: torch.Tensor, max_q_len: int, lse: torch.Tensor, weights: torch.Tensor,
                          scale: Optional[float] = None, causal: bool = True, workspace: Optional[torch.Tensor] = None,
@@ -720,35 +542,20 @@ def fa_paged_key_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: to
     """Adds to weights (B, Hkv, width) float32 the attention weight that each cached key received from
     the new tokens q, lse being what fa_fwd_paged_chunk returned for them. Returns weights. `workspace`
     (uint8, of fa_paged_key_weights_workspace(...) bytes) is allocated by the call unless given."""
-    if _elsewhere(q, stream):
+    if stream is not None:
         with _on_stream(q, stream):
             return fa_paged_key_weights(q, k_cache, block_table, cu_seqlens, kv_lens, max_q_len, lse, weights, scale, causal,
                                         workspace)
-    dev, num, table = _paged_args(k_cache, None, block_table, kv_lens)
-    _packed_args(q, k_cache, cu_seqlens, num, dev)
-    if not q.is_contiguous():
-        raise ValueError("q must be contiguous")
-    total, Hq, D = q.shape
-    Hkv = k_cache.shape[2]
-    _plain("lse", lse, torch.float32, dev)
-    if lse.dim() != 2 or lse.shape[0] != Hq or lse.shape[1] != total:
-        raise ValueError("lse must be (Hq, total)")
-    _key_weights_args(weights, num, Hkv, dev)
-    L = lib()
-    if workspace is None:
-        size = L.fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len)
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    else:
-        _cuda_contig("workspace", workspace)
-        _same_device(q, workspace)
-        size = workspace.numel() * workspace.element_size()
-    st = L.fa_paged_key_weights(q.data_ptr(), k_cache.data_ptr(), *table, cu_seqlens.data_ptr(), kv_lens.data_ptr(), num, total,
-                                max_q_len, lse.data_ptr(), weights.data_ptr(), weights.shape[2], _ptr(workspace), size, Hq, Hkv,
-                                D, scale if scale else 0.0, causal, _dtype_code(q), _current_raw_stream(dev))
+    st = _binding().paged_key_weights(q, k_cache, block_table, cu_seqlens, kv_lens, int(max_q_len), lse, weights,
+                                      float(scale) if scale else 0.0, bool(causal), workspace)
     if st:
         raise FAError(st, "fa_paged_key_weights")
     return weights
+
+
+def fa_paged_key_weights_workspace(Hq: int, Hkv: int, D: int, max_q_len: int) -> int:
+    """Bytes of fa_paged_key_weights's workspace (0: none)."""
+    return lib().fa_paged_key_weights_workspace(int(Hq), int(Hkv), int(D), int(max_q_len))
 
 
 def fa_paged_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -757,18 +564,11 @@ def fa_paged_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: to
     """Cuts every sequence and key head to `budget` keys: the last `recent` and, of the others, those
     of most accumulated weight (B, Hkv, width). Rows are closed up in place, in their order. Returns
     (kept int32 (B, Hkv, budget): old slots, then -1; new kv_lens; new weights)."""
-    if _elsewhere(k_cache, stream):
+    if stream is not None:
         with _on_stream(k_cache, stream):
             return fa_paged_evict(k_cache, v_cache, block_table, kv_lens, weights, budget, recent)
-    dev, num, table = _paged_args(k_cache, v_cache, block_table, kv_lens)
-    Hkv, D = k_cache.shape[2], k_cache.shape[3]
-    _key_weights_args(weights, num, Hkv, dev)
-    kept = torch.empty((num, Hkv, max(0, budget)), dtype=torch.int32, device=k_cache.device)
-    new_lens = torch.empty_like(kv_lens)
-    new_weights = torch.empty_like(weights)
-    st = lib().fa_paged_evict(k_cache.data_ptr(), v_cache.data_ptr(), *table, kv_lens.data_ptr(), weights.data_ptr(),
-                              weights.shape[2], budget, recent, kept.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(),
-                              num, Hkv, D, _dtype_code(k_cache), _current_raw_stream(dev))
+    st, kept, new_lens, new_weights = _binding().paged_evict(k_cache, v_cache, block_table, kv_lens, weights, int(budget),
+                                                             int(recent))
     if st:
         raise FAError(st, "fa_paged_evict")
     return kept, new_lens, new_weights
