@@ -79,18 +79,25 @@ __device__ __forceinline__ int64_t div_up_or_down(int64_t a, int64_t b, bool up)
     return a / b;
 }
 
-// Where a CTA's run begins: the item in which cost `lo` falls, whose own steps begin at cost `pos`.
-// The run takes the steps that begin in [lo, hi); `per` is hi - lo of a whole run.
+// Where a CTA's run begins: the item in which cost `lo` falls, which begins at cost `pos`; an item costs
+// ITEM (loading Q, the epilogue), then its steps. The run takes the steps that begin in [lo, hi); `per` is
+// hi - lo of a whole run. (Without ITEM, CTAs whose runs hold several short items ended 35 % later
+// than those with one: 9 sequences of up to 333 tokens over 2777.)
 struct ChunkStart {
     int b, h, t;
     int64_t pos, lo, hi, per;
 };
 
+// Cost of an item: its tile begins at token i.
+template <int TILES, int BN, int ITEM, bool CAUSAL>
+__device__ __forceinline__ int64_t item_cost(const ChunkSeq &s, int T, int i) {
+    return ITEM + (static_cast<int64_t>(tile_steps<BN, CAUSAL>(s, i + T)) << step_shift<TILES>(s, T, i));
+}
 // Cost of one key head of a sequence.
-template <int TILES, int BN, bool CAUSAL>
+template <int TILES, int BN, int ITEM, bool CAUSAL>
 __device__ __forceinline__ int64_t head_cost(const ChunkSeq &s, int T) {
     int64_t sum = 0;
-    for (int i = 0; i < s.n; i += T) sum += tile_steps<BN, CAUSAL>(s, i + T) << step_shift<TILES>(s, T, i);
+    for (int i = 0; i < s.n; i += T) sum += item_cost<TILES, BN, ITEM, CAUSAL>(s, T, i);
     return sum;
 }
 
@@ -102,7 +109,7 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 
 // One warp finds CTA cta's run (out: shared memory, written by one lane). Each lane takes four
 // consecutive sequences at a time, so up to 128 sequences cost one round of loads.
-template <int TILES, int BN, bool CAUSAL>
+template <int TILES, int BN, int ITEM, bool CAUSAL>
 __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int ctas, ChunkStart *out) {
     constexpr int PER = 4;
     const int lane = threadIdx.x & 31, T = p.tile_tokens;
@@ -115,7 +122,7 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (base + lane * PER + i >= p.num_seqs) s[i].n = 0;
-            cost[i] = head_cost<TILES, BN, CAUSAL>(s[i], T) * p.Hkv;
+            cost[i] = head_cost<TILES, BN, ITEM, CAUSAL>(s[i], T) * p.Hkv;
             mine += cost[i];
         }
     };
@@ -158,7 +165,7 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
             int64_t pos = at + h * one;
             int t = 0;
             for (int i = 0;; i += T, ++t) {
-                const int64_t n = static_cast<int64_t>(tile_steps<BN, CAUSAL>(s, i + T)) << step_shift<TILES>(s, T, i);
+                const int64_t n = item_cost<TILES, BN, ITEM, CAUSAL>(s, T, i);
                 if (start < pos + n) break;
                 pos += n;
             }
@@ -170,7 +177,7 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
 
 // A role's walk over its CTA's run: item after item, each the key tiles [j0, j1) of one row tile
 // (tokens [i0, i0 + tokens) of the sequence).
-template <int TILES, int BN, bool CAUSAL>
+template <int TILES, int BN, int ITEM, bool CAUSAL>
 struct ChunkWalk {
     ChunkSeq s;
     int b, h, i0, j0, j1, steps, keys, tokens, shift;
@@ -186,7 +193,8 @@ struct ChunkWalk {
         pos = st.pos;
         s = chunk_seq(p, b);
         set(p);
-        return j0 < steps || next(p);  // lo may fall behind the start of the item's last step
+        if (j0 >= steps) return next(p);  // lo falls behind the start of the item's last step
+        return j1 > j0;
     }
     __device__ __forceinline__ void set(const ChunkParams &p) {
         keys = tile_keys<CAUSAL>(s, i0 + p.tile_tokens);
@@ -194,12 +202,12 @@ struct ChunkWalk {
         tokens = min(p.tile_tokens, s.n - i0);
         shift = step_shift<TILES>(s, p.tile_tokens, i0);
         const int64_t round = (1 << shift) - 1;
-        j0 = static_cast<int>(max(int64_t(0), lo - pos + round) >> shift);
-        j1 = static_cast<int>(min(static_cast<int64_t>(steps), (hi - pos + round) >> shift));
+        j0 = static_cast<int>(max(int64_t(0), lo - pos - ITEM + round) >> shift);
+        j1 = static_cast<int>(min(static_cast<int64_t>(steps), max(int64_t(0), hi - pos - ITEM + round) >> shift));
     }
     // moves to the next item; false at the end of the run
     __device__ __forceinline__ bool next(const ChunkParams &p) {
-        pos += static_cast<int64_t>(steps) << shift;
+        pos += ITEM + (static_cast<int64_t>(steps) << shift);
         if (pos >= hi) return false;
         i0 += p.tile_tokens;
         if (i0 >= s.n) {
@@ -213,7 +221,7 @@ struct ChunkWalk {
             }
         }
         set(p);
-        return true;
+        return j1 > j0;  // (the run may end before the item's first step)
     }
     __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == steps; }
     // workspace slot of a piece that is not whole
@@ -221,7 +229,7 @@ struct ChunkWalk {
     // The item begun here, for the joining: its pieces run up to the CTA in whose run its last step
     // begins (a run is at least as long as a step, so none between is empty).
     __device__ __forceinline__ ChunkDesc desc(const ChunkParams &p, int64_t per) const {
-        const int64_t last = pos + (static_cast<int64_t>(steps - 1) << shift);
+        const int64_t last = pos + ITEM + (static_cast<int64_t>(steps - 1) << shift);
         return ChunkDesc{static_cast<int>(div_up_or_down(last, per, false)) - static_cast<int>(blockIdx.x) + 1, s.q0 + i0,
                          tokens, h * p.G};
     }
@@ -242,85 +250,110 @@ __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepc
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Joins the pieces of the item that CTA blockIdx.x began and did not finish: m = max of the pieces', l
-// and O summed with each piece scaled by 2^(m_i - m). A warp takes 32 rows (R = 16: 16 rows, two
-// columns side by side) and 8 columns of them: a piece's column is one coalesced load, and those of four
-// pieces are in flight (32 columns a warp and one piece at a time took 29 us for 16 items of 9
-// pieces; the sum of an item's pieces is latency, not bytes). Launched with programmatic dependence: it waits on the device for the attention
-// kernel's end, so its launch costs no gap.
+// and O summed with each piece scaled by 2^(m_i - m). A lane takes four neighbouring rows (one 16-byte load
+// of a column), a warp LR * 4 rows and CL columns at a load; several pieces' loads are in flight, and a
+// piece past the last is the last once more with the scale 0, so that no load waits for a branch (what the
+// joining takes is latency: one load after another, it took 6 us for four pieces of 16 rows and 20 us for
+// two of 256). Launched with programmatic dependence: it waits on the device for the attention kernel's
+// end, so its launch costs no gap.
+template <int D, bool BF16, int R>
+struct CombineCfg {
+    static constexpr int LR = R / 4 < 32 ? R / 4 : 32, CL = 32 / LR;  // lanes for rows, columns of a load
+    static constexpr int LOADS = CL == 1 ? 8 : 4, COLS = CL * LOADS;  // of a warp
+    static constexpr int AHEAD = CL == 1 ? 2 : 4;                     // pieces in flight
+    static constexpr int UNITS = (R / (4 * LR)) * (D / COLS);         // warps' work of a whole tile
+    static_assert(D % COLS == 0, "columns of a warp");
+};
 template <int D, bool BF16, int R>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p) {
-    constexpr int LR = R < 32 ? R : 32, CL = 32 / LR;  // rows of a warp, columns of one load
-    constexpr int COLS = 8, LOADS = COLS / CL;
-    constexpr int UNITS = (R / LR) * (D / COLS);       // warps' work of a whole tile
+    using C = CombineCfg<D, BF16, R>;
+    constexpr int CL = C::CL, LOADS = C::LOADS;
+    const int lane = threadIdx.x & 31, lr = lane % C::LR, cl = lane / C::LR;
+    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int c0 = (unit % (D / C::COLS)) * C::COLS + cl, r0 = (unit / (D / C::COLS)) * (4 * C::LR) + lr * 4;
     pdl_wait();
     const ChunkDesc d = p.desc[blockIdx.x];
-    if (d.pieces < 2) return;
-    const int lane = threadIdx.x & 31, rl = lane % LR, cl = lane / LR;
-    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);
-    if (unit >= UNITS) return;
-    const int half = R / p.mma_tiles;                  // rows of an MMA tile
-    const int c0 = (unit % (D / COLS)) * COLS, r = (unit / (D / COLS)) * LR + rl;
-    // row r of the tile: token and head (rows past the last token of an MMA tile are nobody's)
-    const int T = p.tile_tokens / p.mma_tiles, sub = r / half, rr = r - sub * half;
-    const int ti = rr / p.G, i = sub * T + ti;
-    const bool there = ti < T && i < d.tokens;
-    if (!__any_sync(0xffffffffu, there)) return;
+    if (d.pieces < 2 || unit >= C::UNITS) return;
     auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + k)); };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < d.pieces; ++k) m = fmaxf(m, p.part_ml[slot(k) * R + r].x);
-    if (!there) m = -INFINITY;
-    float acc[LOADS], l = 0.f;
+    auto stats = [&](int k, float *m, float *l) {  // of rows r0 .. r0 + 3
+        const float4 *q = reinterpret_cast<const float4 *>(p.part_ml + slot(k) * R + r0);
+        const float4 a = q[0], b = q[1];
+        m[0] = a.x; l[0] = a.y; m[1] = a.z; l[1] = a.w;
+        m[2] = b.x; l[2] = b.y; m[3] = b.z; l[3] = b.w;
+    };
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    for (int k = 0; k < d.pieces; k += 4) {
+        float x[4][4], l[4];
 #pragma unroll
-    for (int c = 0; c < LOADS; ++c) acc[c] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < d.pieces; ++k) {
-        const float2 ml = p.part_ml[slot(k) * R + r];
-        // a piece in which the row saw nothing adds nothing
-        const float a = m == -INFINITY || ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
-        const float *o = p.part_o + (slot(k) * D + c0 + cl) * R + r;
-        float v[LOADS];
+        for (int q = 0; q < 4; ++q) stats(min(k + q, d.pieces - 1), x[q], l);
 #pragma unroll
-        for (int c = 0; c < LOADS; ++c) v[c] = o[static_cast<int64_t>(c) * CL * R];
-        l = a > 0.f ? fmaf(ml.y, a, l) : l;
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int c = 0; c < LOADS; ++c) acc[c] = fmaf(v[c], a, acc[c]);
+            for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], x[q][i]);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t tok = d.token + i;
-    const int head = d.head + rr - ti * p.G;
-    uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D + c0;
-    if constexpr (CL == 1) {
-        if (there) {
+    float acc[LOADS][4], l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int c = 0; c < COLS; c += 8) {
-                uint32_t x[4];
+    for (int c = 0; c < LOADS; ++c)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float lo = acc[c + 2 * q] * inv, hi = acc[c + 2 * q + 1] * inv;
-                    x[q] = BF16 ? pack2_bf16(lo, hi) : pack2_f16(lo, hi);
-                }
-                *reinterpret_cast<uint4 *>(out + c) = make_uint4(x[0], x[1], x[2], x[3]);
+        for (int i = 0; i < 4; ++i) acc[c][i] = 0.f;
+    for (int k = 0; k < d.pieces; k += C::AHEAD) {
+        float4 v[C::AHEAD][LOADS];
+        float pm[C::AHEAD][4], pl[C::AHEAD][4];
+#pragma unroll
+        for (int q = 0; q < C::AHEAD; ++q) {
+            const int kq = min(k + q, d.pieces - 1);
+            stats(kq, pm[q], pl[q]);
+            const float *o = p.part_o + (slot(kq) * D + c0) * R + r0;
+#pragma unroll
+            for (int c = 0; c < LOADS; ++c) v[q][c] = *reinterpret_cast<const float4 *>(o + c * CL * R);
+        }
+#pragma unroll
+        for (int q = 0; q < C::AHEAD; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // a piece in which the row saw nothing adds nothing
+                const bool none = k + q >= d.pieces || pm[q][i] == -INFINITY;
+                const float a = none ? 0.f : ex2_approx(pm[q][i] - m[i]);
+                if (!none) l[i] = fmaf(pl[q][i], a, l[i]);
+#pragma unroll
+                for (int c = 0; c < LOADS; ++c)
+                    acc[c][i] = fmaf(i == 0 ? v[q][c].x : (i == 1 ? v[q][c].y : (i == 2 ? v[q][c].z : v[q][c].w)), a, acc[c][i]);
+            }
+    }
+    // row r of the tile: token and head (rows past the last token of an MMA tile are nobody's)
+    const int half = R / p.mma_tiles, T = p.tile_tokens / p.mma_tiles;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i, sub = r / half, rr = r - sub * half, ti = rr / p.G, tk = sub * T + ti;
+        if (ti >= T || tk >= d.tokens) continue;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const int64_t tok = d.token + tk;
+        const int head = d.head + rr - ti * p.G;
+        uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D + c0;
+        if constexpr (CL == 1) {
+            uint32_t x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float lo = acc[2 * q][i] * inv, hi = acc[2 * q + 1][i] * inv;
+                x[q] = BF16 ? pack2_bf16(lo, hi) : pack2_f16(lo, hi);
+            }
+            *reinterpret_cast<uint4 *>(out) = make_uint4(x[0], x[1], x[2], x[3]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < LOADS; ++c) {
+                const uint32_t x = BF16 ? pack2_bf16(acc[c][i] * inv, 0.f) : pack2_f16(acc[c][i] * inv, 0.f);
+                out[c * CL] = static_cast<uint16_t>(x);
             }
         }
-    } else {  // this lane holds columns cl, cl + 2, ... of its row
-        static_assert(CL == 1 || CL == 2, "rows of a tile");
-#pragma unroll
-        for (int c = 0; c < LOADS; ++c) {
-            const float other = __shfl_xor_sync(0xffffffffu, acc[c], LR);
-            if (there && cl == 0)
-                *reinterpret_cast<uint32_t *>(out + c * 2) = BF16 ? pack2_bf16(acc[c] * inv, other * inv)
-                                                                  : pack2_f16(acc[c] * inv, other * inv);
-        }
+        if (p.lse && c0 == 0)
+            p.lse[static_cast<int64_t>(head) * p.total + tok] = l[i] > 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
     }
-    if (p.lse && there && c0 == 0 && cl == 0)
-        p.lse[static_cast<int64_t>(head) * p.total + tok] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
 }
 
 template <int D, bool BF16, int R>
 static cudaError_t launch_combine(const ChunkParams &p, int ctas, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, ((R < 32 ? 1 : R / 32) * (D / 8) + 7) / 8, 1);
+    cfg.gridDim = dim3(ctas, (CombineCfg<D, BF16, R>::UNITS + 7) / 8, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 1)
 chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
     using C = RowsCfg<D>;
     constexpr int R = C::R, BN = C::BN, KPW = C::KPW, SW = C::SW, NS = C::NS;
-    using Walk = ChunkWalk<1, BN, CAUSAL>;
+    using Walk = ChunkWalk<1, BN, 0, CAUSAL>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *sO = reinterpret_cast<float *>(smem + C::OFF_O);
@@ -83,7 +83,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    if (warp == 0) chunk_locate<1, BN, CAUSAL>(p, blockIdx.x, gridDim.x, start);
+    if (warp == 0) chunk_locate<1, BN, 0, CAUSAL>(p, blockIdx.x, gridDim.x, start);
     __syncthreads();
     const ChunkStart st = *start;
 

@@ -30,6 +30,7 @@ template <int D>
 struct TileCfg : Cfg<D> {
     using B = Cfg<D>;
     static constexpr int R = B::BM * B::MAXQ;
+    static constexpr int ITEM = 2;  // an item's cost besides its steps (about 2 us; a step of one tile takes 1)
     static constexpr int BARS = 2 + 2 + 2 * B::NS + 2 + 2 + 2 + 2 + 1;
     static constexpr int OFF_START = B::OFF_BAR + BARS * 8;
     static constexpr int OFF_TMEM = OFF_START + static_cast<int>(sizeof(ChunkStart));
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(TileCfg<D>::NUM_THREADS, 1)
 chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const ChunkParams p) {
     using C = TileCfg<D>;
-    using Walk = ChunkWalk<C::MAXQ, C::BN, CAUSAL>;
+    using Walk = ChunkWalk<C::MAXQ, C::BN, C::ITEM, CAUSAL>;
     constexpr int BM = C::BM, BN = C::BN, SW = C::SW, NS = C::NS, U = C::UNITS;
     constexpr bool SINGLE = C::MAXQ == 1, DEC = C::DECOUPLED;
     constexpr int CPB = SW / 16;
@@ -84,7 +85,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();
     }
-    if (warp == 0) chunk_locate<C::MAXQ, BN, CAUSAL>(p, blockIdx.x, gridDim.x, start);
+    if (warp == 0) chunk_locate<C::MAXQ, BN, C::ITEM, CAUSAL>(p, blockIdx.x, gridDim.x, start);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
