@@ -250,16 +250,16 @@ __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepc
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Joins the pieces of the item that CTA blockIdx.x began and did not finish: m = max of the pieces', l
-// and O summed with each piece scaled by 2^(m_i - m). A lane takes four neighbouring rows (one 16-byte load
-// of a column), a warp LR * 4 rows and CL columns at a load; several pieces' loads are in flight, and a
-// piece past the last is the last once more with the scale 0, so that no load waits for a branch (what the
-// joining takes is latency: one load after another, it took 6 us for four pieces of 16 rows and 20 us for
-// two of 256). Launched with programmatic dependence: it waits on the device for the attention kernel's
+// and O summed with each piece scaled by 2^(m_i - m), the maximum running as in the attention itself. A lane
+// takes four neighbouring rows (one 16-byte load of a column), a warp LR * 4 rows and CL columns at a load;
+// the loads of several pieces are issued together, before anything is known of the pieces (what the joining
+// takes is latency: one load after another, it took 6 us for four pieces of 16 rows and 20 us for two of
+// 256). Launched with programmatic dependence: it waits on the device for the attention kernel's
 // end, so its launch costs no gap.
 template <int D, bool BF16, int R>
 struct CombineCfg {
     static constexpr int LR = R / 4 < 32 ? R / 4 : 32, CL = 32 / LR;  // lanes for rows, columns of a load
-    static constexpr int LOADS = CL == 1 ? 8 : 4, COLS = CL * LOADS;  // of a warp
+    static constexpr int LOADS = CL == 1 ? 8 : 2, COLS = CL * LOADS;  // of a warp
     static constexpr int AHEAD = CL == 1 ? 2 : 4;                     // pieces in flight
     static constexpr int UNITS = (R / (4 * LR)) * (D / COLS);         // warps' work of a whole tile
     static_assert(D % COLS == 0, "columns of a warp");
@@ -281,21 +281,14 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p)
         m[0] = a.x; l[0] = a.y; m[1] = a.z; l[1] = a.w;
         m[2] = b.x; l[2] = b.y; m[3] = b.z; l[3] = b.w;
     };
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    for (int k = 0; k < d.pieces; k += 4) {
-        float x[4][4], l[4];
+    float m[4], l[4] = {0.f, 0.f, 0.f, 0.f}, acc[LOADS][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) stats(min(k + q, d.pieces - 1), x[q], l);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], x[q][i]);
-    }
-    float acc[LOADS][4], l[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 4; ++i) m[i] = -INFINITY;
 #pragma unroll
     for (int c = 0; c < LOADS; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[c][i] = 0.f;
+#pragma unroll 1
     for (int k = 0; k < d.pieces; k += C::AHEAD) {
         float4 v[C::AHEAD][LOADS];
         float pm[C::AHEAD][4], pl[C::AHEAD][4];
@@ -311,13 +304,15 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p)
         for (int q = 0; q < C::AHEAD; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // a piece in which the row saw nothing adds nothing
-                const bool none = k + q >= d.pieces || pm[q][i] == -INFINITY;
-                const float a = none ? 0.f : ex2_approx(pm[q][i] - m[i]);
-                if (!none) l[i] = fmaf(pl[q][i], a, l[i]);
+                // a piece in which the row saw nothing (or that was read twice) adds nothing
+                if (k + q >= d.pieces || pm[q][i] == -INFINITY) continue;
+                const float to = fmaxf(m[i], pm[q][i]);
+                const float a0 = ex2_approx(m[i] - to), a1 = ex2_approx(pm[q][i] - to);  // (2^-inf = 0 at the first)
+                m[i] = to;
+                l[i] = fmaf(l[i], a0, pl[q][i] * a1);
 #pragma unroll
                 for (int c = 0; c < LOADS; ++c)
-                    acc[c][i] = fmaf(i == 0 ? v[q][c].x : (i == 1 ? v[q][c].y : (i == 2 ? v[q][c].z : v[q][c].w)), a, acc[c][i]);
+                    acc[c][i] = fmaf(acc[c][i], a0, a1 * (i == 0 ? v[q][c].x : (i == 1 ? v[q][c].y : (i == 2 ? v[q][c].z : v[q][c].w))));
             }
     }
     // row r of the tile: token and head (rows past the last token of an MMA tile are nobody's)
@@ -331,13 +326,16 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p)
         const int head = d.head + rr - ti * p.G;
         uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D + c0;
         if constexpr (CL == 1) {
-            uint32_t x[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float lo = acc[2 * q][i] * inv, hi = acc[2 * q + 1][i] * inv;
-                x[q] = BF16 ? pack2_bf16(lo, hi) : pack2_f16(lo, hi);
+            for (int c = 0; c < LOADS; c += 4) {
+                uint32_t x[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float lo = acc[c + 2 * q][i] * inv, hi = acc[c + 2 * q + 1][i] * inv;
+                    x[q] = BF16 ? pack2_bf16(lo, hi) : pack2_f16(lo, hi);
+                }
+                *reinterpret_cast<uint2 *>(out + c) = make_uint2(x[0], x[1]);
             }
-            *reinterpret_cast<uint4 *>(out) = make_uint4(x[0], x[1], x[2], x[3]);
         } else {
 #pragma unroll
             for (int c = 0; c < LOADS; ++c) {
