@@ -419,6 +419,12 @@ CHUNK = [  # new tokens, keys, hq, hk, D, page, dtype, causal
     ([40, 150], [333, 150], 2, 1, 256, 256, "bf16", True),
     ([64], [200], 7, 1, 256, 16, "fp16", False),
     ([260, 3], [261, 700], 2, 2, 128, 32, "bf16", True),
+    # one row tile, its key tiles split between two warpgroups: 1, 2, 3, many of them, an odd and an even count
+    ([20, 9, 31, 25, 18], [100, 256, 300, 1300, 129], 4, 1, 128, 64, "bf16", True),
+    ([20, 1, 1, 40, 1], [640, 770, 128, 900, 1], 6, 3, 64, 16, "fp16", True),
+    ([33, 70, 18], [1025, 130, 20], 2, 2, 32, 32, "bf16", False),
+    ([17], [2100], 5, 1, 64, 128, "bf16", True),
+    ([300, 20, 129, 1], [600, 520, 257, 900], 2, 1, 128, 16, "bf16", True),  # two tiles and one by turns
 ]
 
 

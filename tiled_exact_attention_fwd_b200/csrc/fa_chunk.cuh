@@ -107,13 +107,29 @@ __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
     return v;
 }
 
-// One warp finds CTA cta's run (out: shared memory, written by one lane). Each lane takes four
-// consecutive sequences at a time, so up to 128 sequences cost one round of loads.
+__device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+
+// One warp finds CTA cta's run (out: shared memory, written by one lane). A few sequences (long prompts: many
+// tiles each) are gone through one by one, a lane per tile; many (a serving batch) with four consecutive
+// sequences per lane, so that up to 128 cost one round of loads. (A lane per sequence took 2 us more
+// for one sequence of 32 tiles.)
 template <int TILES, int BN, int ITEM, bool CAUSAL>
 __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int ctas, ChunkStart *out) {
-    constexpr int PER = 4;
+    constexpr int PER = 4, FEW = 8;
     const int lane = threadIdx.x & 31, T = p.tile_tokens;
+    const bool few = p.num_seqs <= FEW;
     int64_t cost[PER], total = 0, mine = 0;
+    ChunkSeq own = chunk_seq(p, min(lane, p.num_seqs - 1));  // few: sequence `lane`
+    auto seq_of = [&](int b) {
+        return ChunkSeq{__shfl_sync(0xffffffffu, own.q0, b), __shfl_sync(0xffffffffu, own.n, b), __shfl_sync(0xffffffffu, own.kv, b)};
+    };
     auto costs = [&](int base) {
         mine = 0;
         ChunkSeq s[PER];
@@ -126,28 +142,56 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
             mine += cost[i];
         }
     };
-    for (int base = 0; base < p.num_seqs; base += 32 * PER) {
-        costs(base);
-        total += warp_sum64(mine);
+    if (few) {  // mine: cost of a key head of sequence `lane`
+        for (int b = 0; b < p.num_seqs; ++b) {
+            const ChunkSeq s = seq_of(b);
+            int64_t sum = 0;
+            for (int i = lane * T; i < s.n; i += 32 * T) sum += item_cost<TILES, BN, ITEM, CAUSAL>(s, T, i);
+            sum = warp_sum64(sum);
+            total += sum * p.Hkv;
+            if (lane == b) mine = sum;
+        }
+    } else {
+        for (int base = 0; base < p.num_seqs; base += 32 * PER) {
+            costs(base);
+            total += warp_sum64(mine);
+        }
     }
     if (cta == 0)
         for (int b = lane; b < p.num_seqs; b += 32) chunk_check(p, b);
     int64_t per = div_up_or_down(total, ctas, true);
     if (per < p.min_cost) per = p.min_cost;
-    const int64_t start = per * cta;
+    const int64_t start = per * cta, end = min(start + per, total);
     if (start >= total) {
         if (lane == 0) *out = ChunkStart{0, 0, 0, 0, 0, 0, per};
         return;
     }
     int64_t before = 0;
+    if (few) {
+        for (int b = 0; b < p.num_seqs; ++b) {
+            const int64_t one = __shfl_sync(0xffffffffu, mine, b);
+            if (start >= before + one * p.Hkv) {
+                before += one * p.Hkv;
+                continue;
+            }
+            const ChunkSeq s = seq_of(b);
+            const int64_t h = div_up_or_down(start - before, one, false);
+            int64_t pos = before + h * one;
+            for (int t0 = 0; t0 * static_cast<int64_t>(T) < s.n; t0 += 32) {
+                const int i = (t0 + lane) * T;
+                const int64_t c = i < s.n ? item_cost<TILES, BN, ITEM, CAUSAL>(s, T, i) : 0;
+                const int64_t incl = warp_scan64(c, lane), at = pos + incl - c;
+                if (start >= at && start < at + c) *out = ChunkStart{b, static_cast<int>(h), t0 + lane, at, start, end, per};
+                pos += __shfl_sync(0xffffffffu, incl, 31);
+                if (start < pos) break;
+            }
+            break;
+        }
+        return;
+    }
     for (int base = 0; base < p.num_seqs; base += 32 * PER) {
         if (p.num_seqs > 32 * PER) costs(base);
-        int64_t incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
+        const int64_t incl = warp_scan64(mine, lane);
         int64_t at = before + incl - mine;  // cost before this lane's sequences
         if (start >= at && start < at + mine) {
             int b = base + lane * PER;
@@ -169,7 +213,7 @@ __device__ __forceinline__ void chunk_locate(const ChunkParams &p, int cta, int 
                 if (start < pos + n) break;
                 pos += n;
             }
-            *out = ChunkStart{b, static_cast<int>(h), t, pos, start, min(start + per, total), per};
+            *out = ChunkStart{b, static_cast<int>(h), t, pos, start, end, per};
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
@@ -181,16 +225,16 @@ template <int TILES, int BN, int ITEM, bool CAUSAL>
 struct ChunkWalk {
     ChunkSeq s;
     int b, h, i0, j0, j1, steps, keys, tokens, shift;
-    int64_t pos, lo, hi;
+    int64_t pos;
+    const ChunkStart *run;  // in shared memory
     // false when the CTA has no work
-    __device__ __forceinline__ bool begin(const ChunkParams &p, const ChunkStart &st) {
-        lo = st.lo;
-        hi = st.hi;
-        if (lo >= hi) return false;
-        b = st.b;
-        h = st.h;
-        i0 = st.t * p.tile_tokens;
-        pos = st.pos;
+    __device__ __forceinline__ bool begin(const ChunkParams &p, const ChunkStart *st) {
+        run = st;
+        if (st->lo >= st->hi) return false;
+        b = st->b;
+        h = st->h;
+        i0 = st->t * p.tile_tokens;
+        pos = st->pos;
         s = chunk_seq(p, b);
         set(p);
         if (j0 >= steps) return next(p);  // lo falls behind the start of the item's last step
@@ -202,13 +246,13 @@ struct ChunkWalk {
         tokens = min(p.tile_tokens, s.n - i0);
         shift = step_shift<TILES>(s, p.tile_tokens, i0);
         const int64_t round = (1 << shift) - 1;
-        j0 = static_cast<int>(max(int64_t(0), lo - pos - ITEM + round) >> shift);
-        j1 = static_cast<int>(min(static_cast<int64_t>(steps), max(int64_t(0), hi - pos - ITEM + round) >> shift));
+        j0 = static_cast<int>(max(int64_t(0), run->lo - pos - ITEM + round) >> shift);
+        j1 = static_cast<int>(min(static_cast<int64_t>(steps), max(int64_t(0), run->hi - pos - ITEM + round) >> shift));
     }
     // moves to the next item; false at the end of the run
     __device__ __forceinline__ bool next(const ChunkParams &p) {
         pos += ITEM + (static_cast<int64_t>(steps) << shift);
-        if (pos >= hi) return false;
+        if (pos >= run->hi) return false;
         i0 += p.tile_tokens;
         if (i0 >= s.n) {
             i0 = 0;
@@ -228,9 +272,9 @@ struct ChunkWalk {
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (j0 == 0 ? 1 : 0); }
     // The item begun here, for the joining: its pieces run up to the CTA in whose run its last step
     // begins (a run is at least as long as a step, so none between is empty).
-    __device__ __forceinline__ ChunkDesc desc(const ChunkParams &p, int64_t per) const {
+    __device__ __forceinline__ ChunkDesc desc(const ChunkParams &p) const {
         const int64_t last = pos + ITEM + (static_cast<int64_t>(steps - 1) << shift);
-        return ChunkDesc{static_cast<int>(div_up_or_down(last, per, false)) - static_cast<int>(blockIdx.x) + 1, s.q0 + i0,
+        return ChunkDesc{static_cast<int>(div_up_or_down(last, run->per, false)) - static_cast<int>(blockIdx.x) + 1, s.q0 + i0,
                          tokens, h * p.G};
     }
 };
@@ -245,6 +289,66 @@ __device__ __forceinline__ int chunk_page_row(const ChunkParams &p, int b, int p
     }
     return (pg << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
 }
+
+// A producer warp's walk over the key tiles of its CTA's run, one tile ahead in the block table: lane i holds
+// the cache row of the tile's position i << piece_log (2^piece_log rows, which lie in one page). The table's entries of the
+// next tile are asked for before the current one's copies are issued; looked up when they were needed,
+// they cost half a microsecond a part, more than a small tile's arithmetic.
+template <typename Walk, int BN>
+struct ChunkTiles {
+    Walk w;
+    int h, valid, row, piece_log;  // the current tile: key head, its keys, this lane's cache row
+    int j, ahead;
+    bool more, bad;
+    __device__ __forceinline__ ChunkTiles(const ChunkParams &p, const ChunkStart *run, int log) : piece_log(log), bad(false) {
+        more = w.begin(p, run);
+        j = more ? w.j0 : 0;
+        look(p);
+    }
+    __device__ __forceinline__ void look(const ChunkParams &p) {
+        const int in = (threadIdx.x & 31) << piece_log, pos = j * BN + in;
+        ahead = more && in < BN && pos < w.keys ? __ldg(p.block_table + static_cast<int64_t>(w.b) * p.max_blocks + (pos >> p.page_shift)) : 0;
+    }
+    // takes the next tile; false at the end of the run
+    __device__ __forceinline__ bool take(const ChunkParams &p) {
+        if (!more) return false;
+        h = w.h;
+        valid = min(BN, w.keys - j * BN);
+        int pg = ahead;
+        if (pg < 0 || pg >= p.num_pages) {
+            bad = true;
+            pg = 0;
+        }
+        row = (pg << p.page_shift) + ((j * BN + ((threadIdx.x & 31) << piece_log)) & ((1 << p.page_shift) - 1));
+        if (++j >= w.j1) {
+            more = w.next(p);
+            j = more ? w.j0 : 0;
+        }
+        look(p);
+        return true;
+    }
+};
+
+// How a lane takes part in the copies of a tile's part: NB column blocks of ROWS rows in boxes of 2^log rows,
+// one box per lane (there are never more than 16); lanes past the part's boxes copy nothing. All of it is
+// the same for every tile, so a part costs the issuing warp a shuffle and the copy (with the divisions in
+// the loop it took half a microsecond a part, and tiles of D = 64 waited for it).
+template <int NB, int ROWS, int SW>
+struct BoxLane {
+    int log, box, blk, dst, from;  // rows of a box, this lane's box and block, its bytes' place, row's lane
+    __device__ __forceinline__ BoxLane(int page_shift, int piece_log, int r0 = 0) {
+        static_assert((ROWS & (ROWS - 1)) == 0 && (ROWS / 16) * NB <= 32, "a lane per box");
+        const int lane = threadIdx.x & 31;
+        log = min(page_shift, ROWS == 128 ? 7 : 6);
+        static_assert(ROWS == 128 || ROWS == 64, "rows of a part");
+        box = lane / NB;
+        blk = lane % NB;
+        dst = (blk * ROWS + (box << log)) * SW;
+        from = ((r0 + (box << log)) >> piece_log) & 31;
+    }
+    __device__ __forceinline__ int boxes(int have) const { return (min(max(have, 0), ROWS) + (1 << log) - 1) >> log; }
+    __device__ __forceinline__ uint32_t bytes(int n) const { return static_cast<uint32_t>(n << log) * (NB * SW); }
+};
 
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

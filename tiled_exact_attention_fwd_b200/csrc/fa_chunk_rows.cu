@@ -85,38 +85,28 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     }
     if (warp == 0) chunk_locate<1, BN, 0, CAUSAL>(p, blockIdx.x, gridDim.x, start);
     __syncthreads();
-    const ChunkStart st = *start;
 
     if (warp == C::NW) {
         // ------------------------------------------------------------ producer
-        Walk w;
-        bool bad = false, ok = true;
         int u = 0;  // stages filled
         const uint64_t pol = l2_policy_evict_first();
-        const int box = min(1 << p.page_shift, BN);
-        for (bool more = w.begin(p, st); more && ok; more = w.next(p)) {
-            for (int j = w.j0; j < w.j1; ++j, ++u) {
-                const int stage = u % NS;
-                if (u >= NS && !__all_sync(0xffffffffu, wait_bounded(&empty[stage], ((u / NS) - 1) & 1, abort_flag,
-                                                                     p.timeout_ns, 710))) {
-                    ok = false;
-                    break;
-                }
-                const int valid = min(BN, w.keys - j * BN);
-                const int boxes = valid > 0 ? (valid + box - 1) / box : 0;
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], boxes * box * D * 4);
-                __syncwarp();
-                uint8_t *dst = smem + stage * C::STAGE;
-                for (int i = lane; i < boxes * C::NBLK; i += 32) {
-                    const int bx = i / C::NBLK, blk = i % C::NBLK;
-                    const int row = chunk_page_row(p, w.b, j * BN + bx * box, bad);
-                    const int at = blk * BN * SW + bx * box * SW;
-                    tma_load_3d(dst + at, &tm_k, &full[stage], blk * C::SWE, w.h, row, pol);
-                    tma_load_3d(dst + C::TILE + at, &tm_v, &full[stage], blk * C::SWE, w.h, row, pol);
-                }
+        const int log = min(p.page_shift, BN == 64 ? 6 : 7);
+        ChunkTiles<Walk, BN> tiles(p, start, log);
+        const BoxLane<C::NBLK, BN, SW> bl(p.page_shift, log);
+        while (tiles.take(p)) {
+            const int stage = u % NS, n = bl.boxes(tiles.valid), row = __shfl_sync(0xffffffffu, tiles.row, bl.from);
+            if (u >= NS && !__all_sync(0xffffffffu, wait_bounded(&empty[stage], ((u / NS) - 1) & 1, abort_flag, p.timeout_ns, 710)))
+                break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[stage], 2 * bl.bytes(n));
+            __syncwarp();
+            if (bl.box < n) {
+                uint8_t *dst = smem + stage * C::STAGE + bl.dst;
+                tma_load_3d(dst, &tm_k, &full[stage], bl.blk * C::SWE, tiles.h, row, pol);
+                tma_load_3d(dst + C::TILE, &tm_v, &full[stage], bl.blk * C::SWE, tiles.h, row, pol);
             }
+            ++u;
         }
-        if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(FA_ERR_INDEX, 711);
+        if (__any_sync(0xffffffffu, tiles.bad) && lane == 0) record_error(FA_ERR_INDEX, 711);
         if (*abort_flag) {  // the copies in flight land before the shared memory goes away
             for (int v = max(0, u - NS); v < u; ++v) {
                 const uint64_t t0 = global_timer_ns();
@@ -135,7 +125,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         int u = 0;
         ChunkDesc desc{0, 0, 0, 0};
         Walk w;
-        for (bool more = w.begin(p, st); more; more = w.next(p)) {
+        for (bool more = w.begin(p, start); more; more = w.next(p)) {
             // Q rows g and g + 8 of the tile as A fragments
             uint32_t qf[D / 16][4];
             const uint32_t *q0 = nullptr, *q1 = nullptr;
@@ -333,7 +323,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 }
                 consumers_sync();
             }
-            if (w.j0 == 0 && w.j1 < w.steps) desc = w.desc(p, st.per);
+            if (w.j0 == 0 && w.j1 < w.steps) desc = w.desc(p);
         }
         if (threadIdx.x == 0) p.desc[blockIdx.x] = desc;
     }

@@ -11,7 +11,8 @@
 //                   S can be computed meanwhile), O rescaled in TMEM when the maximum grew by 2^8.
 //   warp 8          K/V tiles by TMA, a box per page piece, the lanes issuing side by side.
 //   warp 9          tcgen05.mma: S_t = Q_t K^T, O_t += P_t V, A and B in turn, so that the tensor core
-//                   works on one while the softmax of the other runs. Before an item's last PV it clears
+//                   works on one while the softmax of the other runs. (An item of one row tile: A and B are
+//                   its even and odd key tiles.) Before an item's last PV it clears
 //                   the rows of V past the last key.
 //   warp 10         D <= 64: issues the PVs (warp 9 then the QKs only).
 //   warp 11         Q tiles by TMA, each once the last item's QKs have read its buffer.
@@ -31,11 +32,15 @@ struct TileCfg : Cfg<D> {
     using B = Cfg<D>;
     static constexpr int R = B::BM * B::MAXQ;
     static constexpr int ITEM = 2;  // an item's cost besides its steps (about 2 us; a step of one tile takes 1)
-    static constexpr int BARS = 2 + 2 + 2 * B::NS + 2 + 2 + 2 + 2 + 1;
+    static constexpr int BARS = 2 + 2 + 2 * B::NS + 2 + 2 + 2 + 2 + 1 + 2;
     static constexpr int OFF_START = B::OFF_BAR + BARS * 8;
     static constexpr int OFF_TMEM = OFF_START + static_cast<int>(sizeof(ChunkStart));
     static_assert(BARS * 8 + sizeof(ChunkStart) + 8 <= 512, "barrier area");
-    static_assert(OFF_TMEM + 8 + 1024 <= B::SMEM_BYTES, "shared memory");
+    static constexpr int OFF_ML = B::USED;  // (m, l) of the odd key tiles' rows (128)
+    static constexpr int OFF_WALK = OFF_ML + 1024;  // the softmax warps' walks
+    static constexpr int END = OFF_WALK + B::NUM_SOFTMAX_WARPS * 64 + 1024;
+    static constexpr int SMEM = END > B::SMEM_BYTES ? END : B::SMEM_BYTES;
+    static_assert(OFF_TMEM + 8 <= OFF_ML && SMEM <= 227 * 1024, "shared memory");
 };
 
 template <int D, bool BF16, bool CAUSAL>
@@ -53,6 +58,8 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *q_free = q_full + 2, *kv_full = q_free + 2, *kv_empty = kv_full + NS, *s_full = kv_empty + NS;
     uint64_t *p_full = s_full + 2, *pv_done = p_full + 2, *s_free = pv_done + 2, *drain = s_free + 2;
+    uint64_t *x_full = drain + 1, *x_free = x_full + 1;  // split keys: B's results are there, are read
+    float2 *sML = reinterpret_cast<float2 *>(smem + C::OFF_ML);
     ChunkStart *start = reinterpret_cast<ChunkStart *>(smem + C::OFF_START);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::OFF_TMEM);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::OFF_TMEM + 4);
@@ -75,6 +82,8 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             mbar_init(&kv_empty[s], 1);
         }
         mbar_init(drain, DEC ? 2 : 1);
+        mbar_init(x_full, 128);
+        mbar_init(x_free, 128);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -97,39 +106,41 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         Walk w;
         if (warp == W_TMA) {
             // ------------------------------------------------------------ K/V producer
-            bool bad = false, ok = true;
+            bool ok = true;
             int u = 0;  // ring parts issued
             const uint64_t pol = l2_policy_evict_last();
-            for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
-                for (int j = w.j0; ok && j < w.j1; ++j) {
-                    const int valid = min(BN, w.keys - j * BN);
-                    for (int part = 0; part < 2 * U; ++part, ++u) {
-                        const int stage = u % NS;
-                        if (u >= NS &&
-                            !__all_sync(0xffffffffu, wait_bounded(&kv_empty[stage], ((u / NS) - 1) & 1, abort_flag, lim, 750))) {
-                            ok = false;
-                            break;
-                        }
-                        // part of K_j: some column blocks of all rows; part of V_j: some rows of all blocks
-                        const bool is_v = part >= U;
-                        const int sub = is_v ? part - U : part;
-                        const int rows = is_v ? C::VROWS_PER_UNIT : BN, r0 = is_v ? sub * C::VROWS_PER_UNIT : 0;
-                        const int b0 = is_v ? 0 : sub * C::KBLK_PER_UNIT, nb = is_v ? C::NBLK : C::KBLK_PER_UNIT;
-                        const int box = min(1 << p.page_shift, rows), have = min(rows, valid - r0);
-                        const int boxes = have > 0 ? (have + box - 1) / box : 0;
-                        if (lane == 0) mbar_arrive_expect_tx(&kv_full[stage], boxes * box * nb * SW);
-                        __syncwarp();
-                        uint8_t *dst = sKV + stage * C::UNIT_BYTES;
-                        for (int i = lane; i < boxes * nb; i += 32) {
-                            const int bx = i / nb, blk = i - bx * nb;
-                            const int row = chunk_page_row(p, w.b, j * BN + r0 + bx * box, bad);
-                            tma_load_3d(dst + (blk * rows + bx * box) * SW, is_v ? &tm_v : &tm_k, &kv_full[stage],
-                                        (b0 + blk) * C::SWE, w.h, row, pol);
-                        }
-                    }
+            constexpr int VR = C::VROWS_PER_UNIT, KB = C::KBLK_PER_UNIT;
+            const int log = min(p.page_shift, VR == 64 ? 6 : 7);
+            ChunkTiles<Walk, BN> tiles(p, start, log);
+            const BoxLane<KB, BN, SW> bk(p.page_shift, log);      // a part of K_j: KB column blocks of all rows
+            const BoxLane<C::NBLK, VR, SW> bv(p.page_shift, log);  // a part of V_j: VR rows of all blocks
+            auto begin = [&](int stage, uint32_t bytes) {
+                if (u >= NS && !__all_sync(0xffffffffu, wait_bounded(&kv_empty[stage], ((u / NS) - 1) & 1, abort_flag, lim, 750)))
+                    return false;
+                if (lane == 0) mbar_arrive_expect_tx(&kv_full[stage], bytes);
+                __syncwarp();
+                return true;
+            };
+            while (ok && tiles.take(p)) {
+                const int nk = bk.boxes(tiles.valid), row_k = __shfl_sync(0xffffffffu, tiles.row, bk.from);
+#pragma unroll
+                for (int sub = 0; sub < U; ++sub, ++u) {
+                    const int stage = u % NS;
+                    if (!(ok = ok && begin(stage, bk.bytes(nk)))) break;
+                    if (bk.box < nk)
+                        tma_load_3d(sKV + stage * C::UNIT_BYTES + bk.dst, &tm_k, &kv_full[stage], (sub * KB + bk.blk) * C::SWE,
+                                    tiles.h, row_k, pol);
+                }
+#pragma unroll
+                for (int sub = 0; sub < U; ++sub, ++u) {
+                    const int stage = u % NS, nv = bv.boxes(tiles.valid - sub * VR);
+                    const int row_v = __shfl_sync(0xffffffffu, tiles.row, (bv.from + ((sub * VR) >> log)) & 31);
+                    if (!(ok = ok && begin(stage, bv.bytes(nv)))) break;
+                    if (bv.box < nv)
+                        tma_load_3d(sKV + stage * C::UNIT_BYTES + bv.dst, &tm_v, &kv_full[stage], bv.blk * C::SWE, tiles.h, row_v, pol);
                 }
             }
-            if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(FA_ERR_INDEX, 751);
+            if (__any_sync(0xffffffffu, tiles.bad) && lane == 0) record_error(FA_ERR_INDEX, 751);
             if (*abort_flag) {  // the copies in flight land before the shared memory goes away
                 for (int v = max(0, u - NS); v < u; ++v) {
                     const uint64_t t0 = global_timer_ns();
@@ -146,14 +157,14 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 if (ok) ok = __all_sync(0xffffffffu, wait_bounded(bar, ph, abort_flag, lim, where));
                 return ok;
             };
-            // S_t = Q_t K_jj^T; `first`: the first tile to use this K, `last`: the last
-            auto qk = [&](int t, int jj, bool first, bool last, bool item_end) {
-                const int gs = (t ? gb : ga) + jj, buf = SINGLE ? (gs & 1) : t;
-                if (jj == 0 && !wait(&q_full[t], nq[t] & 1, 760 + t)) return;
+            // S_t = Q_qt K_jj^T, the tile's step ts; `first`: the first tile to use this K, `last`: the last
+            auto qk = [&](int t, int qt, int jj, int ts, bool first, bool last, bool item_end) {
+                const int gs = (t ? gb : ga) + ts, buf = SINGLE ? (gs & 1) : t;
+                if (jj == 0 && !wait(&q_full[qt], nq[qt] & 1, 760 + qt)) return;
                 if (DEC && gs > 0 && !wait(&s_free[t], (gs - 1) & 1, 762 + t)) return;
                 tc_fence_after_sync();
                 constexpr uint32_t idesc = idesc_f16(BM, BN, BF16, false), dhi = smem_desc_hi(8 * SW, C::LAYOUT);
-                const uint32_t q_lo = smem_desc_lo(smem_u32(sQ + t * C::Q_BYTES), 16);
+                const uint32_t q_lo = smem_desc_lo(smem_u32(sQ + qt * C::Q_BYTES), 16);
                 constexpr int UK = D / 16 / U;
 #pragma unroll
                 for (int un = 0; un < U; ++un) {
@@ -173,12 +184,12 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                     if (un + 1 == U) umma_commit_elect(&s_full[buf]);
                     if (last) umma_commit_elect(&kv_empty[stage]);
                 }
-                if (item_end) umma_commit_elect(&q_free[t]);
+                if (item_end) umma_commit_elect(&q_free[qt]);
             };
             // O_t += P_t V_jj; valid < BN: V_jj's rows from `valid` on are past the last key and are
             // cleared first (what the page or the ring holds there may be NaN, and 0 NaN = NaN)
-            auto pv = [&](int t, int jj, bool first, bool last, int valid) {
-                const int gs = (t ? gb : ga) + jj, buf = SINGLE ? (gs & 1) : t;
+            auto pv = [&](int t, int jj, int ts, bool first, bool last, int valid) {
+                const int gs = (t ? gb : ga) + ts, buf = SINGLE ? (gs & 1) : t;
                 const int part0 = u0 + (2 * jj + 1) * U;
                 if (first) {
 #pragma unroll
@@ -211,14 +222,14 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
                     for (int kk = 0; kk < UV; ++kk) {
                         const int k = un * UV + kk;
-                        umma_ts_elect(o, a + k * 8, v_lo + ((kk * 16 * SW) >> 4), dhi, idesc, (jj > 0 || k > 0) ? 1u : 0u);
+                        umma_ts_elect(o, a + k * 8, v_lo + ((kk * 16 * SW) >> 4), dhi, idesc, (ts > 0 || k > 0) ? 1u : 0u);
                     }
                     if (un + 1 == U) umma_commit_elect(&pv_done[t]);
                     if (last) umma_commit_elect(&kv_empty[stage]);
                 }
             };
             const bool do_qk = !DEC || warp == W_MMA, do_pv = !DEC || warp == W_PV;
-            for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
+            for (bool more = w.begin(p, start); more && ok; more = w.next(p)) {
                 const int n = w.j1 - w.j0;
                 const bool two = !SINGLE && w.tokens > TT;
                 const int end = w.keys - w.j0 * BN;  // keys of the segment (its last tile may reach past them)
@@ -228,34 +239,33 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                         bool is_v;
                         int j;
                         decode_step(i, n, is_v, j);
-                        if (is_v) pv(0, j, true, true, valid(j));
-                        else qk(0, j, true, true, j == n - 1);
+                        if (is_v) pv(0, j, j, true, true, valid(j));
+                        else qk(0, 0, j, j, true, true, j == n - 1);
                     }
+                    ga += n;
                 } else {
-                    // A and B in turn; separate P buffers: a QK runs one step ahead of the PVs
-                    if (do_qk) qk(0, 0, true, !two, n == 1);
-                    if (do_qk && ok && two) qk(1, 0, false, true, n == 1);
-                    for (int j = 1; ok && j <= n; ++j) {
-                        if (DEC) {
-                            if (do_qk && j < n) qk(0, j, true, !two, j == n - 1);
-                            if (do_qk && ok && two && j < n) qk(1, j, false, true, j == n - 1);
-                            if (do_pv) pv(0, j - 1, true, !two, valid(j - 1));
-                            if (do_pv && ok && two) pv(1, j - 1, false, true, BN);
-                        } else {
-                            pv(0, j - 1, true, !two, valid(j - 1));
-                            if (ok && j < n) qk(0, j, true, !two, j == n - 1);
-                            if (ok && two) pv(1, j - 1, false, true, BN);
-                            if (ok && two && j < n) qk(1, j, false, true, j == n - 1);
+                    // Steps of A and B in turn, the QKs two ahead of the PVs. Two row tiles: A and B of key tile o / 2;
+                    // one: key tile o, the even ones through A, the odd ones through B. (One loop for both: each
+                    // copy of an issue is a hundred instructions, and more of them than the instruction cache
+                    // holds beside the softmax made short items 12 % slower.)
+                    const int N = two ? 2 * n : n;
+#pragma unroll 1
+                    for (int o = -2; ok && o < N; ++o) {
+                        if (do_pv && o >= 0) {
+                            const int t = o & 1, j = two ? o >> 1 : o;
+                            pv(t, j, o >> 1, !two || t == 0, !two || t == 1, valid(j));
+                        }
+                        if (do_qk && ok && o + 2 < N) {
+                            const int t = o & 1, j = two ? (o + 2) >> 1 : o + 2;
+                            qk(t, two ? t : 0, j, (o + 2) >> 1, !two || t == 0, !two || t == 1, j == n - 1);
                         }
                     }
+                    ga += (N + 1) >> 1;
+                    gb += N >> 1;
+                    if (two) nq[1]++;
                 }
                 u0 += 2 * U * n;
-                ga += n;
                 nq[0]++;
-                if (two) {
-                    gb += n;
-                    nq[1]++;
-                }
             }
             umma_commit_elect(drain);
             const uint64_t t0 = global_timer_ns();
@@ -269,7 +279,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 bool ok = true;
                 int nq[2] = {0, 0};
                 const uint64_t pol = l2_policy_evict_first();
-                for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
+                for (bool more = w.begin(p, start); more && ok; more = w.next(p)) {
                     const bool two = !SINGLE && w.tokens > TT;
                     for (int t = 0; t < (two ? 2 : 1); ++t) {
                         if (nq[t] > 0 && !wait_bounded(&q_free[t], (nq[t] - 1) & 1, abort_flag, lim, 770 + t)) {
@@ -301,22 +311,42 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const uint32_t o_addr = tmem + lane_base + C::O_COL + t * D;
         const float sc = p.scale_log2;
         bool ok = true;
-        int gbase = 0;
-        ChunkDesc desc{0, 0, 0, 0};
+        int gbase = 0, splits = 0;  // steps of this tile; items with split keys
+        bool owe = false;           // B: the last such item's results may not have been read yet
+        // The walk waits in shared memory while an item's steps run: these warps are at their register limit
+        // there (kept in registers it spills into the loop: 192 -> 223 us at D = 64, 2048 tokens over 8192).
+        static_assert(sizeof(Walk) <= 64, "a walk's place");
+        Walk *const parked = reinterpret_cast<Walk *>(smem + C::OFF_WALK + warp * 64);
+        if (threadIdx.x == 0) p.desc[blockIdx.x] = ChunkDesc{0, 0, 0, 0};
         Walk w;
 #pragma unroll 1
-        for (bool more = w.begin(p, *start); more; more = w.next(p)) {
-            if (w.j0 == 0 && w.j1 < w.steps) desc = w.desc(p, start->per);
-            if (t == 1 && w.tokens <= TT) continue;  // tile absent
-            const int n = w.j1 - w.j0;
-            const int rows = min(w.tokens - t * TT, TT) * p.G;  // of this MMA tile
-            const bool row_ok = r < rows;
-            const bool busy = quarter * 32 < rows;  // this warp has a row
-            // keys this row sees, counted from the segment's first
-            int hi = (row_ok ? token_keys<CAUSAL>(w.s, w.i0 + t * TT + r / p.G) : w.keys) - w.j0 * BN;
+        for (bool more = w.begin(p, start); more; more = w.next(p)) {
+            if (threadIdx.x == 0 && w.j0 == 0 && w.j1 < w.steps) p.desc[blockIdx.x] = w.desc(p);
+            // With one row tile in the item A and B share it, A taking the segment's even key tiles and B the odd
+            // ones, each with its own (m, l) and O (one tile alone would wait for itself at every step: 1.4 us
+            // a step against 1.7 for two); A joins them at the end.
+            bool busy;        // this warp has a row
+            int n, hi, stride;  // this warpgroup's steps; keys this row sees, counted from its first key tile
+            {
+                const bool split = !SINGLE && w.tokens <= TT;
+                n = split ? (w.j1 - w.j0 + 1 - t) >> 1 : w.j1 - w.j0;
+                if (n == 0) continue;
+                const int first = split ? 0 : t * TT;              // the tile's first token
+                const int rows = min(w.tokens - first, TT) * p.G;  // of this MMA tile
+                busy = quarter * 32 < rows;
+                stride = split ? 2 * BN : BN;
+                hi = (r < rows ? token_keys<CAUSAL>(w.s, w.i0 + first + r / p.G) : w.keys) - (w.j0 + (split ? t : 0)) * BN;
+                __syncwarp();
+                if (lane == 0) *parked = w;
+                __syncwarp();
+            }
+            if (owe) {  // O_B is written again from this item's first PV on
+                owe = false;
+                if (ok) ok = __all_sync(0xffffffffu, wait_bounded(x_free, (splits - 1) & 1, abort_flag, lim, 790));
+            }
             float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int jj = 0; ok && jj < n; ++jj, hi -= BN) {
+            for (int jj = 0; ok && jj < n; ++jj, hi -= stride) {
                 const int gs = gbase + jj, buf = SINGLE ? (gs & 1) : t;
                 const uint32_t ph = (SINGLE ? (gs >> 1) : gs) & 1;
                 if (!__all_sync(0xffffffffu, wait_bounded(&s_full[buf], ph, abort_flag, lim, 780 + t))) {
@@ -414,22 +444,61 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             }
             if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&pv_done[t], (gbase + n - 1) & 1, abort_flag, lim, 788 + t));
             gbase += n;
-            if (!ok || !busy) continue;
+            w = *parked;
+            const bool split = !SINGLE && w.tokens <= TT, joins = split && w.j1 - w.j0 > 1;
+            const int first = split ? 0 : t * TT;
+            const bool row_ok = r < min(w.tokens - first, TT) * p.G;
+            float scale_a = 1.f, scale_b = 0.f;
+            if (joins) {
+                ++splits;
+                if (t == 1) {  // B: (m, l) to A, which reads O_B out of TMEM
+                    if (!ok) continue;
+                    sML[r] = make_float2(m, l);
+                    tc_fence_before_sync();
+                    mbar_arrive(x_full);
+                    owe = true;
+                    continue;
+                }
+                if (ok) ok = __all_sync(0xffffffffu, wait_bounded(x_full, (splits - 1) & 1, abort_flag, lim, 792));
+                if (ok) {
+                    const float2 b = sML[r];
+                    const float to = fmaxf(m, b.x);
+                    scale_a = m == -INFINITY ? 0.f : ex2_approx(m - to);
+                    scale_b = b.x == -INFINITY ? 0.f : ex2_approx(b.x - to);
+                    m = to;
+                    l = l * scale_a + b.y * scale_b;
+                }
+            }
+            if (!ok) continue;
             tc_fence_after_sync();
+            if (!busy) {
+                if (joins) mbar_arrive(x_free);
+                continue;
+            }
             const bool whole = w.whole();
             const int ti = r / p.G;
-            const int64_t tok = w.s.q0 + w.i0 + t * TT + ti;
+            const int64_t tok = w.s.q0 + w.i0 + first + ti;
             const int head = w.h * p.G + r - ti * p.G;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D;
             const int64_t slot = w.slot();
-            float *po = p.part_o + slot * D * C::R + t * BM + r;  // column by column
+            const int pr = split ? r : t * BM + r;              // row of the item's tile
+            float *po = p.part_o + slot * D * C::R + pr;        // column by column
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld32(o_addr + c0, o);
                 tmem_ld_wait();
                 tmem_reg_fence<32>(o);
+                if (joins) {
+                    uint32_t x[32];
+                    tmem_ld32(o_addr + D + c0, x);  // O_B
+                    tmem_ld_wait();
+                    tmem_reg_fence<32>(x);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        o[k] = __float_as_uint(fmaf(__uint_as_float(o[k]), scale_a, __uint_as_float(x[k]) * scale_b));
+                }
                 if (!whole) {
 #pragma unroll
                     for (int v = 0; v < 32; ++v) po[(c0 + v) * C::R] = __uint_as_float(o[v]);
@@ -449,12 +518,15 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                 }
                 __syncwarp();
             }
+            if (joins) {
+                tc_fence_before_sync();
+                mbar_arrive(x_free);
+            }
             if (!whole)
-                p.part_ml[slot * C::R + t * BM + r] = make_float2(m, l);
+                p.part_ml[slot * C::R + pr] = make_float2(m, l);
             else if (row_ok && p.lse)
                 p.lse[static_cast<int64_t>(head) * p.total + tok] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
         }
-        if (threadIdx.x == 0) p.desc[blockIdx.x] = desc;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -483,11 +555,11 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
             if (fa_attr.numRegs * C::NUM_THREADS < 128 * C::regs_low(false) + 256 * C::regs_high(false))
                 return cudaErrorInvalidConfiguration;
         }
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         __atomic_fetch_or(&attr_set_mask, bit, __ATOMIC_RELEASE);
     }
-    kern<<<ctas, C::NUM_THREADS, C::SMEM_BYTES, st>>>(tq, tk, tv, p);
+    kern<<<ctas, C::NUM_THREADS, C::SMEM, st>>>(tq, tk, tv, p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_combine<D, BF16, C::R>(p, ctas, st);
 }
