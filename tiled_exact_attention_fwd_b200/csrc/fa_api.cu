@@ -73,7 +73,8 @@ bool head_dim_ok(int D) { return D == 32 || D == 64 || D == 128 || D == 256; }
 
 // Token-major (N, H, D) 16-bit tensor seen by TMA as dims (D, H, N); one box is
 // `inner` elements of one head of `rows` consecutive tokens (a [rows][inner] tile).
-bool encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows) {
+bool encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows,
+                CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     EncodeTiledFn f = encode_fn();
     if (!f) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
@@ -84,7 +85,7 @@ bool encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64
     const CUtensorMapSwizzle sw = (inner * 2 == 128) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     const CUresult r = f(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                          const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
@@ -94,8 +95,10 @@ namespace fa {
 uint64_t host_wait_limit_ns() { return wait_limit_ns(); }
 int host_sm_count() { return sm_count(); }
 bool host_head_dim_ok(int D) { return head_dim_ok(D); }
-bool host_encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows) {
-    return encode_map(m, base, bf16, D, H, N, inner, rows);
+bool host_encode_pool_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows) {
+    return encode_map(m, base, bf16, D, H, N, inner, rows,
+                      D >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                               : (D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B));
 }
 bool host_encode_group_map(CUtensorMap *m, const void *base, bool bf16, int D, int G, int Hkv, int64_t N, int inner,
                            int tokens) {

@@ -257,8 +257,8 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     p.out_align32 = aligned(out, 32);
     CUtensorMap tk, tv;
     const int64_t rows = static_cast<int64_t>(num_pages) * page_size;
-    if (!fa::host_encode_map(&tk, k_cache, bf16, D, Hkv, rows, inner, k_box) ||
-        !fa::host_encode_map(&tv, v_cache, bf16, D, Hkv, rows, inner, v_box))
+    if (!fa::host_encode_pool_map(&tk, k_cache, bf16, D, Hkv, rows, inner, k_box) ||
+        !fa::host_encode_pool_map(&tv, v_cache, bf16, D, Hkv, rows, inner, v_box))
         return FA_ERR_CUDA;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (few) return done(fa::launch_chunk_rows(D, bf16, causal != 0, tk, tv, p, ctas, cs));
@@ -300,7 +300,7 @@ fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int inner = fa::fwd_box_inner_elems(D);
     CUtensorMap tk, tq;
-    if (!fa::host_encode_map(&tk, k_cache, bf16, D, Hkv, static_cast<int64_t>(num_pages) * page_size, inner,
+    if (!fa::host_encode_pool_map(&tk, k_cache, bf16, D, Hkv, static_cast<int64_t>(num_pages) * page_size, inner,
                              fa::key_weights_box(page_size)))
         return FA_ERR_CUDA;
     if (few) return done(fa::launch_key_weights(D, bf16, causal != 0, tk, p, ctas, cs));

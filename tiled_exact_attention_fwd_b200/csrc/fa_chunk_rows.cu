@@ -5,13 +5,13 @@
 // its group shares, so with up to 16 rows the time is that of the bytes; what the kernel needs is
 // loads in flight and an SM that never waits for arithmetic. One CTA per SM walks an equal run of
 // the steps of all items (fa_chunk.cuh):
-//   warp 4       producer: brings K and V tiles of BN keys through an NS-stage ring by TMA, a box
-//                per page piece, the lanes issuing a tile's boxes side by side; ~190 KB in flight.
-//   warps 0-3    each takes BN / 4 keys of every tile by itself: S = Q K^T and O += P V with
+//   last warp    producer: brings K and V tiles of BN keys through an NS-stage ring by TMA, a box
+//                per page piece, the lanes issuing a tile's boxes side by side.
+//   consumers    (4 warps, 8 at D <= 64) each takes 16 keys of every tile by itself: S = Q K^T and O += P V with
 //                mma.sync m16n8k16 (16 rows fill the tile; a 128-row tcgen05 tile would compute 8 to
 //                128 times the rows there are, and its softmax would run one row per thread), its
 //                own running (m, l) and its own O in registers, so that warps meet only at the
-//                end of an item, where the four are joined through shared memory.
+//                end of an item, where they are joined through shared memory.
 // The running maximum is in log2 units and moves only when it grows by more than 2^8 (the final
 // 1/l cancels it exactly); P is rounded to the input type for the second product, the sums l take
 // the unrounded values; all statistics and O are 32-bit.
@@ -34,15 +34,17 @@ namespace {
 template <int D>
 struct RowsCfg {
     static constexpr int R = 16;
-    static constexpr int NW = 4;                     // consumer warps
-    static constexpr int KPW = D <= 64 ? 32 : 16;    // keys a warp takes of a tile
+    static constexpr int NW = D <= 64 ? 8 : 4;       // consumer warps
+    static constexpr int KPW = 16;                   // keys a warp takes of a tile
     static constexpr int BN = NW * KPW;
     static constexpr int SW = (2 * D >= 128) ? 128 : 2 * D;
     static constexpr int SWE = SW / 2;
     static constexpr int NBLK = D / SWE;
     static constexpr int TILE = BN * D * 2;          // bytes of a K (or V) tile
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int NS = STAGE >= 65536 ? 3 : (STAGE >= 32768 ? 6 : 8);
+    // 128 KB on the way (192 at D = 256, whose stages are 64 KB): with more, the memory's rate falls (64 single
+    // tokens over 8192, D = 128: 192 KB 216 us, 160 KB 208, 128 KB 207).
+    static constexpr int NS = STAGE >= 65536 ? 3 : (STAGE >= 32768 ? 4 : 8);
     static constexpr int DH = D < 128 ? D : 128;     // columns of O joined at a time
     static constexpr int OROW = DH + 4;              // floats; keeps the 8 rows of a store apart in the banks
     static constexpr int OFF_O = NS * STAGE;
@@ -55,7 +57,10 @@ struct RowsCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 template <int D, bool BF16, bool CAUSAL>
 __global__ void __launch_bounds__(RowsCfg<D>::THREADS, 1)
@@ -251,7 +256,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage]);
             }
-            // ---- join the four warps' rows
+            // ---- join the warps' rows
             l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
             l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
             l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
@@ -262,7 +267,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
             const bool whole = w.whole();
             const int rows = w.tokens * p.G;
-            const int row = threadIdx.x >> 3, col8 = threadIdx.x & 7;  // 8 threads a row
+            constexpr int TPR = 2 * C::NW;                             // threads a row
+            const int row = threadIdx.x / TPR, col8 = threadIdx.x % TPR;
 #pragma unroll
             for (int half = 0; half < D / C::DH; ++half) {
                 constexpr int NT = C::DH / 8;
@@ -274,7 +280,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     if (g + 8 < rows)
                         *reinterpret_cast<float2 *>(sO + (warp * R + g + 8) * C::OROW + i * 8 + 2 * t4) = make_float2(oi[2], oi[3]);
                 }
-                consumers_sync();
+                consumers_sync<32 * C::NW>();
                 if (row < rows) {
                     float m = -INFINITY, l = 0.f, a[C::NW];
 #pragma unroll
@@ -292,8 +298,9 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     const int64_t slot = w.slot();
                     float *po = p.part_o + (slot * D + half * C::DH) * R + row;
 #pragma unroll
-                    for (int c = 0; c < C::DH / 32; ++c) {
-                        const int col = c * 32 + col8 * 4;
+                    for (int c = 0; c < (C::DH + 4 * TPR - 1) / (4 * TPR); ++c) {
+                        const int col = c * (4 * TPR) + col8 * 4;
+                        if (col >= C::DH) break;
                         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int v = 0; v < C::NW; ++v) {
@@ -321,7 +328,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                                 l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
                     }
                 }
-                consumers_sync();
+                consumers_sync<32 * C::NW>();
             }
             if (w.j0 == 0 && w.j1 < w.steps) desc = w.desc(p);
         }

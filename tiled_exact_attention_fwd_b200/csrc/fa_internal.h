@@ -8,12 +8,13 @@
 namespace fa {
 
 // Host helpers of fa_api.cu shared by the C-ABI sources: the bound of every wait, the current
-// device's SM count (-1: error), the supported head dims, and the TMA map of a token-major (N, H, D)
-// 16-bit tensor with boxes of `inner` elements of one head of `rows` tokens.
+// device's SM count (-1: error), the supported head dims, and the TMA map of a page pool, a token-major
+// (N, H, D) 16-bit tensor with boxes of `inner` elements of one head of `rows` tokens (L2 fetches no more
+// than a head's row: of the next head's it would read bytes that another CTA may want much later).
 uint64_t host_wait_limit_ns();
 int host_sm_count();
 bool host_head_dim_ok(int D);
-bool host_encode_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows);
+bool host_encode_pool_map(CUtensorMap *m, const void *base, bool bf16, int D, int H, int64_t N, int inner, int rows);
 // The same tensor with its heads in Hkv groups of G: boxes of `inner` elements of one group's G heads of
 // `tokens` tokens (rows token-major, the group's heads within a token).
 bool host_encode_group_map(CUtensorMap *m, const void *base, bool bf16, int D, int G, int Hkv, int64_t N, int inner,
