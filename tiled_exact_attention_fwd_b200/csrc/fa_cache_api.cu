@@ -4,7 +4,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
-#include <stdlib.h>
 #include <stdint.h>
 
 #include "fa.h"
@@ -334,7 +333,6 @@ fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_tabl
     p.capacity = capacity_of(max_blocks_per_seq, page_size);
     p.Hkv = Hkv; p.D = D;
     p.weights = weights; p.width = width; p.budget = budget; p.recent = recent;
-    if (getenv("EVS")) p.slice = atoi(getenv("EVS"));
     p.kept = kept; p.new_lens = new_lens; p.new_weights = new_weights;
     return done(fa::launch_evict(p, static_cast<cudaStream_t>(stream)));
 }

@@ -3,9 +3,9 @@
 //
 // Select. Of n > budget keys the last `recent` stay, and of the others the budget - recent of
 // most weight, the lowest slot first where weights are equal. One CTA per (sequence, key head): the
-// weight of rank k is found by a radix select over the order-preserving image of the float (four
-// passes of 8 bits, histograms in shared memory, one copy per warp group against contention),
-// then one pass in slot order writes the kept slots, with block-wide prefix sums over "kept" and
+// weight of rank k is found by a radix select over the order-preserving image of the float (11, 11 and 10
+// bits, histograms in shared memory: with the exponent's last bits in the first digit few threads meet in a
+// bin), then one pass in slot order writes the kept slots, with block-wide prefix sums over "kept" and
 // "equal to the threshold". Everything is counted in integers: the result does not depend on
 // the order of the threads.
 //
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelItems = 4;   // consecutive slots per thread
-constexpr int kHistCopies = 8;
+constexpr int kHistCopies = 2, kBins = 2048;
 constexpr int kSelHeld = 16;   // images held in a thread's registers over the passes (the rest is read again)
 
 // Order-preserving image: a > b as floats <=> image(a) > image(b); -0 equals 0, NaN is above +inf.
@@ -62,9 +62,10 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, 
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictParams p) {
-    __shared__ uint32_t hist[kHistCopies][256];
+    __shared__ __align__(8) uint32_t hist[kHistCopies][kBins];
     __shared__ uint32_t warp_sums[32];
     __shared__ uint32_t s_digit, s_rank;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the moving CTAs may wait beside these
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     const int64_t bh = static_cast<int64_t>(b) * p.Hkv + h;
     const float *w = p.weights + bh * p.width;
@@ -92,43 +93,35 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictPa
             const int i = q * kSelThreads + tid;
             held[q] = i < old ? weight_image(w[i]) : 0u;
         }
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < kHistCopies * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), above = pass == 1 ? 21 : 10;  // 11, 11, 10 bits
+            const uint32_t digits = pass == 2 ? 1023u : 2047u;
+            for (int i = tid; i < kHistCopies * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
             __syncthreads();
             uint32_t *mine = hist[(tid >> 5) % kHistCopies];
-            auto count = [&](uint32_t x, bool valid) {
-                if (shift == 24) {
-                    // the top byte (sign and exponent) takes few values: one addition per value and warp
-                    const uint32_t d = valid ? x >> 24 : 256u;
-                    const uint32_t peers = __match_any_sync(0xffffffffu, d);
-                    if (valid && (threadIdx.x & 31) == __ffs(peers) - 1) atomicAdd(&mine[d], __popc(peers));
-                } else if (valid && (x >> (shift + 8)) == (prefix >> (shift + 8))) {
-                    atomicAdd(&mine[(x >> shift) & 255], 1u);
-                }
+            auto count = [&](uint32_t x) {
+                if (pass == 0 || (x >> above) == (prefix >> above)) atomicAdd(&mine[(x >> shift) & digits], 1u);
             };
 #pragma unroll
             for (int q = 0; q < kSelHeld; ++q)
-                if (q * kSelThreads < old) count(held[q], q * kSelThreads + tid < old);
-            for (int i0 = kSelHeld * kSelThreads; i0 < old; i0 += kSelThreads)
-                count(i0 + tid < old ? weight_image(w[i0 + tid]) : 0u, i0 + tid < old);
+                if (q * kSelThreads + tid < old) count(held[q]);
+            for (int i = kSelHeld * kSelThreads + tid; i < old; i += kSelThreads) count(weight_image(w[i]));
             __syncthreads();
-            if (tid < 256) {  // thread d takes digit 255 - d: ranks from the largest digit down
-                uint32_t c = 0;
+            // thread t takes digits 2 (1023 - t) + 1 and 2 (1023 - t): ranks from the largest digit down
+            uint32_t c[2] = {0, 0};
 #pragma unroll
-                for (int q = 0; q < kHistCopies; ++q) c += hist[q][255 - tid];
-                uint32_t incl = c;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
-                    if ((tid & 31) >= o) incl += x;
-                }
-                if ((tid & 31) == 31) warp_sums[tid >> 5] = incl;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                for (int i = 0; i < (tid >> 5); ++i) incl += warp_sums[i];
-                if (incl - c < rank && rank <= incl) {
-                    s_digit = 255 - tid;
-                    s_rank = rank - (incl - c);
-                }
+            for (int q = 0; q < kHistCopies; ++q) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(&hist[q][2 * (kSelThreads - 1 - tid)]);
+                c[0] += v.y;
+                c[1] += v.x;
+            }
+            uint32_t total;
+            const uint32_t before = block_scan(c[0] + c[1], warp_sums, total);
+            if (before < rank && rank <= before + c[0] + c[1]) {
+                const bool first = rank <= before + c[0];
+                s_digit = 2 * (kSelThreads - 1 - tid) + (first ? 1 : 0);
+                s_rank = rank - before - (first ? 0 : c[0]);
             }
             __syncthreads();
             prefix |= s_digit << shift;
@@ -283,10 +276,14 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
     evict_select_kernel<<<dim3(p.Hkv, p.batch), kSelThreads, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int which = p.slice ? p.slice : 64;
-    if (which >= 256 && p.D >= 128) return launch_move<256>(p, st);
-    if (which >= 128 && p.D >= 64) return launch_move<128>(p, st);
-    return launch_move<64>(p, st);
+    // Wider slices are kinder to the memory, narrower ones make more CTAs. 8192 keys cut to 2048, D = 128, slices of
+    // 32 / 64 / 128 / 256 bytes (us): 64 sequences of 8 heads 345 / 263 / 258 / 247, 16 of 8 90 / 74.7 / 72.8 /
+    // 85.9, 2 of 8 25.5 / 28.9 / 40.7 / 60.2.
+    const int64_t bytes = static_cast<int64_t>(p.batch) * p.Hkv * p.D * 4;  // of all heads' K and V rows
+    if (bytes >= 1024 * 256 && p.D >= 128) return launch_move<256>(p, st);
+    if (bytes >= 512 * 128 && p.D >= 64) return launch_move<128>(p, st);
+    if (bytes >= 256 * 64) return launch_move<64>(p, st);
+    return launch_move<32>(p, st);
 }
 
 cudaError_t evict_error_addrs(int **code, int **where) { return device_error_addrs(code, where); }

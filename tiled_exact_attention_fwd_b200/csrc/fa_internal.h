@@ -203,7 +203,6 @@ struct EvictParams {
     const float *weights;                       // (batch, Hkv, width)
     int64_t width;
     int budget, recent;
-    int slice;
     int32_t *kept, *new_lens;                   // (batch, Hkv, budget), (batch)
     float *new_weights;                         // as weights
 };

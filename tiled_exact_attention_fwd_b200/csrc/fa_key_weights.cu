@@ -148,7 +148,9 @@ struct KeyWalk {
 template <int D>
 struct KeyCfg {
     static constexpr int R = 16;                   // rows a step
-    static constexpr int NW = 4, KPW = 32;         // consumer warps, keys of each
+    // consumer warps (at D <= 64 four did not keep up with the memory: 95 us, eight 68, for 64 single tokens
+    // over 8192), keys of each
+    static constexpr int NW = D <= 64 ? 8 : 4, KPW = 32;
     static constexpr int BN = NW * KPW;
     static constexpr int SW = (2 * D >= 128) ? 128 : 2 * D;
     static constexpr int SWE = SW / 2, NBLK = D / SWE;
