@@ -312,9 +312,10 @@ FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const vo
  *                share key head h.
  *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
  *                of (page_size, Hkv, D). Entries past ceil(kv_lens[b] / page_size) are never read;
- *                what a page holds past the sequence's last key does not matter (NaN included).
- *   kv_lens      device int32 [num_seqs]: keys of each sequence, the new tokens' own included.
- *                Sequences may share pages.
+ *                what a page holds past the sequence's last key does not matter (NaN included). A value
+ *                of V within it that is not finite reaches rows that do not see its key too (0 times it).
+ *   kv_lens      device int32 [num_seqs]: keys of each sequence, the new tokens' own included, at most
+ *                2^31 - 2^16. Sequences may share pages.
  *   causal       nonzero: new token i of n sees keys 0 .. kv_lens[b] - n + i (aligned at the end);
  *                zero: all of them. A row that sees no key gets out = 0 and lse = -inf.
  *   max_q_len    the most new tokens of a sequence. It chooses the kernel and the workspace's size, not the
@@ -370,8 +371,8 @@ FA_API fa_status fa_paged_key_weights(const void *q, const void *k_cache, const 
  *   kept         int32 (B, Hkv, budget) output: the old slot of each kept key, rising, then -1.
  *   new_lens     int32 [B] output: min(kv_lens[b], budget).
  *   new_weights  float32 (B, Hkv, width) output: the kept keys' weights in their new slots, zeros after.
- * 1 <= budget <= width < 2^31, 0 <= recent <= budget. new_weights and new_lens are not weights and kv_lens
- * themselves. Lengths that do not fit the table are cut to it and FA_ERR_INDEX is left for fa_device_status;
+ * 1 <= budget <= width <= 2^31 - 2^16, 0 <= recent <= budget. The outputs overlap neither weights nor kv_lens
+ * (FA_ERR_SHAPE) nor one another. Lengths that do not fit the table are cut to it and FA_ERR_INDEX is left for fa_device_status;
  * a row whose table entry is outside the pool does not move (FA_ERR_INDEX too).
  */
 FA_API fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_table,

@@ -195,6 +195,16 @@ class TestRefusals:
     def test_evict(self, lib, change, status):
         assert self.evict(lib, **change) == status
 
+    # the inputs at 1 << 20 (weights: 2 * 2 * 64 * 4 = 1024 bytes) and 1 << 21 (lengths: 8 bytes)
+    @pytest.mark.parametrize("change", [
+        dict(nw=(1 << 20) + 1020), dict(nw=(1 << 20) - 1020), dict(kept=(1 << 20) + 512), dict(kept=(1 << 20) - 124),
+        dict(nl=(1 << 20) + 4), dict(nl=(1 << 21) + 4), dict(kept=(1 << 21) - 4), dict(nw=(1 << 21) - 1000),
+        dict(width=(1 << 31) - 1, mb=1 << 26)])
+    def test_evict_overlaps(self, lib, change):
+        a = dict(w=1 << 20, kv=1 << 21, kept=1 << 22, nl=1 << 23, nw=1 << 24)
+        a.update(change)
+        assert self.evict(lib, **a) == -2
+
 
 # --------------------------------------------------------------------------- norm and rotation
 def norm_inputs(tokens, hq, hk, D, rot, dtype, wtype, fused, seed):
@@ -603,3 +613,242 @@ def test_a_cache_s_life(cuda_device, hq, hk, D, dtype):
             assert torch.equal(c.cpu().view(torch.int16), w.view(torch.int16))
         lens = kv.tolist()
     assert fa.fa_device_status()[0] == 0
+
+
+# --------------------------------------------------------------------------- batches, streams, graphs
+def check_chunk_and_weights(dev, new, kv, hq, hk, D, page, dtype, seed, max_q=None):
+    import tiled_exact_attention_fwd_b200 as fa
+    dt, max_q = DT[dtype], max(new) if max_q is None else max_q
+    q, kc, vc, bt, cu, lens = chunk_inputs(new, kv, hq, hk, D, page, dtype, seed, behind=0)
+    args = [t.to(dev) for t in (q, kc, vc, bt, cu, lens)]
+    out, lse = fa.fa_fwd_paged_chunk(*args, max_q)
+    ref, rl, size, ssize = oc.chunk_attention(q, kc, vc, bt, cu, lens)
+    e = score_tol(ssize)
+    within(out, ref, half_step(dt) * ref.abs() + (half_step(dt) + 2 * e.t()[..., None]) * size + 2.0 ** -25, "out")
+    within(lse, rl, e + 2.0 ** -23 * rl.abs(), "lse")
+    w = torch.zeros(len(kv), hk, bt.shape[1] * page, device=dev)
+    fa.fa_paged_key_weights(args[0], args[1], *args[3:], max_q, lse, w)
+    add, most = oc.key_weights(q, kc, bt, cu, lens, lse.cpu(), w.shape[2])
+    within(w, add, (2.0 ** -19 * (most + 1) + 1024 * U) * add, "weights")
+    assert fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("count", [8, 9, 33, 128, 129, 300])
+@pytest.mark.parametrize("few", [True, False])
+def test_many_sequences(cuda_device, count, few):
+    """The split's ways over a batch: one by one, in one round of loads, in several."""
+    g = fa_inputs.generator(count)
+    new = torch.randint(0, 3, (count,), generator=g) if few else torch.tensor([0, 1, 40, 90])[torch.randint(0, 4, (count,), generator=g)]
+    new[-1] = 1 if few else 40
+    kv = (new + torch.randint(0, 150, (count,), generator=g)).tolist()
+    check_chunk_and_weights(cuda_device, new.tolist(), kv, 6, 2, 64, 16, "bf16", 41 + count)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new,kv,max_q", [([20, 1, 7], [90, 300, 7], 1), ([1, 2, 1], [400, 33, 17], 4000)])
+def test_max_q_len_does_not_change_the_result(cuda_device, new, kv, max_q):
+    check_chunk_and_weights(cuda_device, new, kv, 8, 2, 128, 16, "bf16", 5, max_q)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,hq,hk", [(64, 128, 1), (32, 20, 1), (128, 34, 2), (256, 96, 3)])
+def test_many_heads_a_key_head(cuda_device, D, hq, hk):
+    check_chunk_and_weights(cuda_device, [1, 3, 0, 9], [200, 3, 50, 300], hq, hk, D, 32, "fp16", 51)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [[1, 1, 1], [30, 1, 2]])
+def test_outputs_of_any_allowed_alignment(cuda_device, new):
+    """out 16 but not 32 bytes from a boundary, lse 4; the caller's workspace full of NaN, or too small."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev = cuda_device
+    q, kc, vc, bt, cu, lens = chunk_inputs(new, [700, 40, 129], 4, 2, 64, 16, "bf16", 61, behind=0)
+    args = [t.to(dev) for t in (q, kc, vc, bt, cu, lens)]
+    want, wl = fa.fa_fwd_paged_chunk(*args, max(new))
+    out = torch.empty(q.numel() + 8, dtype=q.dtype, device=dev)[8:].view(q.shape)
+    lse = torch.empty(wl.numel() + 1, device=dev)[1:].view(wl.shape)
+    size = fa.fa_fwd_paged_chunk_workspace(4, 2, 64, max(new))
+    ws = torch.full((size // 4,), float("nan"), device=dev)
+    fa.fa_fwd_paged_chunk(*args, max(new), out=out, lse=lse, workspace=ws)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_paged_chunk(*args, max(new), workspace=ws[:-1])
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_paged_chunk(*args, max(new), workspace=ws.view(torch.uint8)[16:])
+    for bad in (dict(out=out.half()), dict(out=out[:1]), dict(lse=lse[:1]), dict(lse=lse.t().contiguous()), dict(workspace=ws.cpu())):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_paged_chunk(*args, max(new), **bad)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_paged_chunk(args[0].transpose(0, 1), *args[1:], max(new))
+    with pytest.raises(ValueError):
+        fa.fa_fwd_paged_chunk(*args[:5], args[5].long(), max(new))
+    with pytest.raises(ValueError):
+        fa.fa_fwd_paged_chunk(*args[:4], args[4][:-1], args[5], max(new))
+    with pytest.raises(ValueError):
+        fa.fa_paged_key_weights(args[0], args[1], *args[3:], max(new), wl, torch.zeros(3, 2, 8, device=dev).double())
+    with pytest.raises(fa.FAError):
+        fa.fa_paged_key_weights(args[0], args[1], *args[3:], max(new), wl, torch.zeros(3, 2, 8, device=dev))
+    with pytest.raises(ValueError):
+        fa.fa_paged_evict(args[1], args[2], args[3], args[5], torch.zeros(3, 1, 4096, device=dev), 4, 0)
+
+
+class Step:
+    """One step of a serving loop on buffers of its own: append, attention, weights, eviction."""
+
+    def __init__(self, dev, new, kv, hq, hk, D, seed):
+        self.new, self.max_q = new, max(new)
+        total, page = sum(new), 16
+        _, kc, vc, bt, cu, lens = chunk_inputs(new, kv, hq, hk, D, page, "bf16", seed, behind=0)
+        self.pools = [torch.nan_to_num(t, 1.0).to(dev) for t in (kc, vc)]
+        self.kc, self.vc = (t.clone() for t in self.pools)
+        self.bt, self.cu, self.lens = bt.to(dev), cu.to(dev), lens.to(dev)
+        self.x = [fa_inputs.normal((total, h, D), torch.bfloat16, seed + i).to(dev) for i, h in enumerate((hq, hk, hk))]
+        self.wq, self.cs = weights_of(D, torch.bfloat16, seed).to(dev), angles(4096, D).to(dev)
+        self.pos = torch.arange(total, device=dev)
+        self.w = torch.zeros(len(kv), hk, bt.shape[1] * page, device=dev)
+
+    def reset(self):
+        self.kc.copy_(self.pools[0]), self.vc.copy_(self.pools[1]), self.w.zero_()
+
+    def run(self, stream=None):
+        import tiled_exact_attention_fwd_b200 as fa
+        q = fa.fa_qk_norm_rope_paged(*self.x, self.wq, self.wq, self.cs, self.pos, self.kc, self.vc, self.bt, self.cu,
+                                     self.lens, stream=stream)
+        out, lse = fa.fa_fwd_paged_chunk(q, self.kc, self.vc, self.bt, self.cu, self.lens, self.max_q, stream=stream)
+        fa.fa_paged_key_weights(q, self.kc, self.bt, self.cu, self.lens, self.max_q, lse, self.w, stream=stream)
+        return [q, out, lse, *fa.fa_paged_evict(self.kc, self.vc, self.bt, self.lens, self.w, 100, 20, stream=stream)]
+
+    def state(self, results):
+        return [t.clone() for t in (*results, self.kc, self.vc, self.w)]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+STEPS = [([1] * 5, [700, 3, 130, 999, 64], 8, 2, 128), ([40, 1, 0, 150], [300, 500, 20, 151], 4, 2, 64)]
+
+
+@pytest.mark.gpu
+def test_captured_and_replayed(cuda_device):
+    """Steps captured into graphs of their own give, replayed in any order and at the same time on two
+    streams, with the inputs changed in place, the bits of eager calls."""
+    steps = [Step(cuda_device, *s, seed=71 + i) for i, s in enumerate(STEPS)]
+    for s in steps:  # first calls outside a capture
+        s.run()
+    graphs, results = [], []
+    for s in steps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            results.append(s.run())
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for turn in range(6):
+        for s in steps:
+            s.x[0].copy_(torch.randn(s.x[0].shape, generator=fa_inputs.generator(turn)))
+            s.reset()
+        wants = []
+        for s in steps:
+            wants.append(s.state(s.run()))
+            s.reset()
+        torch.cuda.synchronize()
+        for i in (0, 1) if turn % 2 else (1, 0):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for s, r, want in zip(steps, results, wants):
+            assert same(s.state(r), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("as_int", [False, True])
+def test_other_streams_and_two_calls_at_once(cuda_device, as_int):
+    steps = [Step(cuda_device, *s, seed=81 + i) for i, s in enumerate(STEPS)]
+    wants = []
+    for s in steps:
+        wants.append(s.state(s.run()))
+        s.reset()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        results = [s.run(stream=st.cuda_stream if as_int else st) for s, st in zip(steps, streams)]
+        torch.cuda.synchronize()
+        for s, r, want in zip(steps, results, wants):
+            assert same(s.state(r), want)
+            s.reset()
+        torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_gradients_captured_beside_an_eager_graph(cuda_device):
+    """The backward captured while eager work on the same tensors goes on."""
+    import tiled_exact_attention_fwd_b200 as fa
+    q, k, v, wq, wk, cs, pos = (None if t is None else on(cuda_device, t) for t in
+                                norm_inputs(300, 4, 2, 64, 64, torch.bfloat16, torch.bfloat16, True, 3))
+    gq, gk = torch.randn_like(q), torch.randn_like(k)
+    want = fa.fa_qk_norm_rope_bwd(q, k, wq, wk, cs, pos, gq, gk)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = fa.fa_qk_norm_rope_bwd(q, k, wq, wk, cs, pos, gq, gk)
+        y = fa.fa_qk_norm_rope(q, k, wq, wk, cs, pos)
+    for _ in range(3):
+        for t in got + y:
+            t.fill_(float("nan"))
+        g.replay()
+        again = fa.fa_qk_norm_rope_bwd(q, k, wq, wk, cs, pos, gq, gk)
+        assert same(got, want) and same(again, want)
+        assert same(y, fa.fa_qk_norm_rope(q, k, wq, wk, cs, pos))
+
+
+# --------------------------------------------------------------------------- long caches
+@pytest.mark.gpu
+@pytest.mark.parametrize("length,budget,recent", [(40000, 17000, 100), (33000, 33000 // 16 * 16, 0), (20000, 1, 1), (16385, 16384, 0)])
+def test_evict_from_long_caches(cuda_device, length, budget, recent):
+    """More keys than the selection holds in registers."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, page, hk, D = cuda_device, 64, 2, 32
+    g = fa_inputs.generator(length)
+    cols = -(-length // page)
+    bt = torch.randperm(cols, generator=g).to(torch.int32)[None]
+    kc, vc = (torch.randn(cols, page, hk, D, generator=g).bfloat16() for _ in range(2))
+    w = torch.randint(0, 500, (1, hk, cols * page), generator=g).float()
+    lens = torch.tensor([length], dtype=torch.int32)
+    kept, new, nw = oc.evict(w, lens, budget, recent)
+    want = [oc.move_rows(c, bt, kept, lens, budget) for c in (kc, vc)]
+    dk, dv = kc.to(dev), vc.to(dev)
+    got = fa.fa_paged_evict(dk, dv, bt.to(dev), lens.to(dev), w.to(dev), budget, recent)
+    assert torch.equal(got[0].cpu(), kept) and torch.equal(got[1].cpu(), new) and torch.equal(got[2].cpu(), nw)
+    assert torch.equal(dk.cpu(), want[0]) and torch.equal(dv.cpu(), want[1])
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(cuda_device):
+    """Pools of 2^31 elements and a few pages more (4.3 GB each): a step whose keys lie in the first and the last pages gives what
+    the same keys give in a small pool."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, page, hq, hk, D = cuda_device, 256, 8, 8, 128
+    pages = 2 ** 31 // (page * hk * D) + 4
+    assert (pages - 4) * page * hk * D >= 2 ** 31
+    lens = torch.tensor([700, 500], dtype=torch.int32, device=dev)
+    small = torch.arange(5, dtype=torch.int32, device=dev)
+    big = torch.tensor([pages - 1, 0, pages - 3, pages - 2, pages - 4], dtype=torch.int32, device=dev)
+    cut = lambda t: torch.stack([t[:3], torch.cat([t[3:], t[:1]])])  # noqa: E731  (the last entry is never read)
+    for new in ([1, 1], [100, 40]):
+        total = sum(new)
+        x = [fa_inputs.normal((total, h, D), torch.bfloat16, i).to(dev) for i, h in enumerate((hq, hk, hk))]
+        cu, cs = fa_inputs.cu_seqlens_from_lengths(new).to(dev), angles(1000, D).to(dev)
+        seen = []
+        for n, order in ((5, small), (pages, big)):
+            kc, vc = (torch.empty(n, page, hk, D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+            for i, c in enumerate((kc, vc)):
+                c[order.long()] = fa_inputs.normal((5, page, hk, D), torch.bfloat16, 90 + i).to(dev)
+            w = torch.zeros(2, hk, 3 * page, device=dev)
+            q = fa.fa_qk_norm_rope_paged(*x, None, None, cs, None, kc, vc, cut(order), cu, lens)
+            out, lse = fa.fa_fwd_paged_chunk(q, kc, vc, cut(order), cu, lens, max(new))
+            fa.fa_paged_key_weights(q, kc, cut(order), cu, lens, max(new), lse, w)
+            res = fa.fa_paged_evict(kc, vc, cut(order), lens, w, 300, 50)
+            seen.append([q, out, lse, w, *res, kc[order.long()], vc[order.long()]])
+            assert fa.fa_device_status()[0] == 0
+            del kc, vc
+        assert same(*seen)

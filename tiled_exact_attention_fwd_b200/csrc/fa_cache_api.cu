@@ -26,9 +26,15 @@ bool pages_ok(int max_blocks, int page_size, int num_pages) {
     return static_cast<int64_t>(num_pages) * page_size <= INT32_MAX;
 }
 
+// Keys that a table row can name: positions, and those of the tile behind them, stay below 2^31.
 int capacity_of(int max_blocks, int page_size) {
     const int64_t c = static_cast<int64_t>(max_blocks) * page_size;
-    return c > INT32_MAX ? INT32_MAX : static_cast<int>(c);
+    return c > fa::kMaxSeqKeys ? fa::kMaxSeqKeys : static_cast<int>(c);
+}
+
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return x < y + nb && y < x + na;
 }
 
 // Up to 128 query heads share a key head (a token's rows lie in one MMA tile).
@@ -319,13 +325,17 @@ fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_tabl
     if (!fa::host_head_dim_ok(D)) return FA_ERR_HEADDIM;
     if (B < 0 || B > 65535 || Hkv <= 0 || Hkv > 65535 || budget <= 0 || recent < 0 || recent > budget) return FA_ERR_SHAPE;
     if (!pages_ok(max_blocks_per_seq, page_size, num_pages)) return FA_ERR_SHAPE;
-    if (width < static_cast<int64_t>(max_blocks_per_seq) * page_size || width > INT32_MAX || budget > width) return FA_ERR_SHAPE;
+    if (width < static_cast<int64_t>(max_blocks_per_seq) * page_size || width > fa::kMaxSeqKeys || budget > width) return FA_ERR_SHAPE;
     if (B == 0) return FA_OK;
     if (!k_cache || !v_cache || !block_table || !kv_lens || !weights || !kept || !new_lens || !new_weights) return FA_ERR_NULL;
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
         !aligned(weights, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(new_weights, 4))
         return FA_ERR_ALIGN;
-    if (weights == new_weights || kv_lens == new_lens) return FA_ERR_SHAPE;  // read again while the results are written
+    // the inputs are read again while the results are written
+    const int64_t heads = static_cast<int64_t>(B) * Hkv, w_bytes = heads * width * 4;
+    const struct { const void *p; int64_t n; } results[3] = {{kept, heads * budget * 4}, {new_lens, int64_t(B) * 4}, {new_weights, w_bytes}};
+    for (const auto &r : results)
+        if (overlap(weights, w_bytes, r.p, r.n) || overlap(kv_lens, int64_t(B) * 4, r.p, r.n)) return FA_ERR_SHAPE;
     fa::EvictParams p{};
     p.k_cache = k_cache; p.v_cache = v_cache;
     p.block_table = block_table; p.kv_lens = kv_lens;

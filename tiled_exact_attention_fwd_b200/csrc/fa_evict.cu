@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 #pragma unroll
         for (int q = 0; q < U; ++q) {
             const int j = j0 + q * RPT + r;
-            src[q] = j < p.budget ? __ldg(kept + j) : j;
+            src[q] = j < p.budget ? __ldcg(kept + j) : j;
         }
 #pragma unroll
         for (int q = 0; q < U; ++q) {

@@ -168,6 +168,7 @@ struct ChunkParams {
     float2 *part_ml;
     float *part_o;
 };
+constexpr int kMaxSeqKeys = 0x7fffffff - 0xffff;  // keys of a sequence in a cache
 constexpr int kChunkMaxCtas = 160;              // the workspace is laid out for this many CTAs
 // Tiles of 16 rows (fa_chunk_rows.cu).
 cudaError_t launch_chunk_rows(int D, bool bf16, bool causal, const CUtensorMap &tk, const CUtensorMap &tv,

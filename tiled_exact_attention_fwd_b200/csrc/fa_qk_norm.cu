@@ -118,8 +118,7 @@ struct Turn {
         s[2] = f2(v.x, v.y);
         s[3] = f2(v.z, v.w);
     }
-    // (xa, xb) turned by the angles, or (BACK) by their negatives, in place
-    template <bool BACK>
+    // (xa, xb) turned by the angles, in place
     __device__ __forceinline__ void apply(uint64_t *xa, uint64_t *xb) const {
         if (INTER) {
 #pragma unroll
@@ -127,14 +126,10 @@ struct Turn {
                 float c0, c1, s0, s1, p, q;
                 f2_split(c[i >> 1], c0, c1);
                 f2_split(s[i >> 1], s0, s1);
-                float ca = (i & 1) ? c1 : c0, sa = (i & 1) ? s1 : s0;
+                const float ca = (i & 1) ? c1 : c0, sa = (i & 1) ? s1 : s0;
                 f2_split(c[2 + (i >> 1)], c0, c1);
                 f2_split(s[2 + (i >> 1)], s0, s1);
-                float cb = (i & 1) ? c1 : c0, sb = (i & 1) ? s1 : s0;
-                if (BACK) {
-                    sa = -sa;
-                    sb = -sb;
-                }
+                const float cb = (i & 1) ? c1 : c0, sb = (i & 1) ? s1 : s0;
                 f2_split(xa[i], p, q);
                 xa[i] = f2(fmaf(p, ca, -(q * sa)), fmaf(q, ca, p * sa));
                 f2_split(xb[i], p, q);
@@ -145,8 +140,8 @@ struct Turn {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint64_t sn = fmul2(s[i], minus), a = xa[i];
-                xa[i] = ffma2(a, c[i], fmul2(xb[i], BACK ? s[i] : sn));
-                xb[i] = ffma2(xb[i], c[i], fmul2(a, BACK ? sn : s[i]));
+                xa[i] = ffma2(a, c[i], fmul2(xb[i], sn));
+                xb[i] = ffma2(xb[i], c[i], fmul2(a, s[i]));
             }
         }
     }
@@ -401,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_fwd_kernel(const QkN
             }
             const float r = rsqrtf(row_sum<LPR>(ssa, ssb) * (1.0f / D) + p.eps);
             const uint64_t r2 = f2(r, r);
-            turn.template apply<false>(xa, xb);
+            turn.apply(xa, xb);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 xa[k] = fmul2(xa[k], r2);
