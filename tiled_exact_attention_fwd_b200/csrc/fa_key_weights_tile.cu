@@ -7,14 +7,20 @@
 // (row, key) at 16 per clock and SM, 1024 clocks per 128 x 128 tile against 64 D / 16 for the MMAs.
 // An item is KT = 2 neighbouring key tiles A and B (one at D = 256) of one (sequence, key head), whose K
 // stays in shared memory while the row tiles pass:
-//   warps 0-3, 4-7  tile A, B: S^T from TMEM, weights 2^(s c - lse), the key's sum
-//   warp 8          K by TMA (page pieces), two buffers (one at D = 256)
-//   warp 9          the MMAs, two S^T buffers per tile
-//   warp 10         Q tiles by TMA through a ring
-//   warp 11         the row tiles' -lse (log2 units) into the ring's stages
+//   warps 0-7, 8-15  tile A, B: S^T from TMEM, weights 2^(s c - lse), the key's sum; four warps a
+//                    half of the columns, 32 in registers at a time (with four a tile, all columns at
+//                    once, two warps a scheduler did not cover one another's waits: 2 x 777 tokens over
+//                    13332 keys, 16 heads on 4, D = 64: 108 us, now 85)
+//   and then one     K by TMA (page pieces), two buffers (one at D = 256)
+//   each for         the MMAs, two S^T buffers per tile
+//                    Q tiles by TMA through a ring
+//                    the row tiles' -lse (log2 units) into the ring's stages
 // The steps (row tiles of items) are cut into runs of equal cost, one per CTA, as in fa_chunk.cuh; an
 // item that a cut falls into leaves partial sums in the workspace, which key_weights_join_kernel adds up
 // in the order of the rows: no atomics, the same call gives the same bits.
+// Measured: 2 x 777 tokens over 3333 keys (16 heads on 4, D = 64) 33 us, of which the smaller half is
+// starting (finding the run, the first tiles) and joining; 2048 tokens over 8192 keys (32 heads on 8, D =
+// 128) 183 us, 2.6 exponentials per ns of 4.5.
 #include "fa_chunk.cuh"
 #include "fa_fwd_kernel.cuh"
 
@@ -30,16 +36,18 @@ struct KtCfg {
     static constexpr uint32_t LAYOUT = (SW == 128) ? kLayoutSw128 : kLayoutSw64;
     static constexpr int TILE = BN * D * 2;         // bytes of a K or Q tile
     static constexpr int K_BYTES = KT * TILE;
-    static constexpr int NQ = D == 256 ? 2 : (D == 128 ? 3 : 4);
+    static constexpr int NQ = D >= 128 ? 2 : 4;
     static constexpr int OFF_Q = KB * K_BYTES;
     static constexpr int OFF_L = OFF_Q + NQ * TILE;  // NQ x 128 floats
-    static constexpr int OFF_BAR = OFF_L + NQ * BN * 4;
+    static constexpr int OFF_SUM = OFF_L + NQ * BN * 4;  // 2 x KEYS floats: the second column half's sums
+    static constexpr int OFF_BAR = OFF_SUM + 2 * KEYS * 4;
     static constexpr int BARS = 2 * KB + 3 * NQ + 4 * KT + 1;
     static constexpr int OFF_START = OFF_BAR + BARS * 8;
     static constexpr int OFF_TMEM = OFF_START + static_cast<int>(sizeof(ChunkStart));
     static constexpr int USED = OFF_TMEM + 8 + 1024;
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA (and its TMEM) per SM
-    static constexpr int NUM_S_WARPS = 4 * KT;
+    static constexpr int COLS = BN / 2;             // columns of a tile that a warp takes
+    static constexpr int NUM_S_WARPS = 8 * KT;
     static constexpr int THREADS = 32 * (NUM_S_WARPS + 4);
     static constexpr uint32_t TMEM_COLS = KT * 256;
     static_assert(USED <= 227 * 1024, "shared memory");
@@ -68,10 +76,18 @@ struct KeyTileWalk {
         for (int j = 0; j * KEYS < s.kv; ++j) sum += item_cost(s, T, tiles, j);
         return sum;
     }
+    // As chunk_locate: a few sequences one by one, a lane per item; many with four per lane. (A lane a sequence took
+    // 6 us for two of 52 items.)
     __device__ static void locate(const ChunkParams &p, int cta, int ctas, ChunkStart *out) {
-        constexpr int PER = 4;
+        constexpr int PER = 4, FEW = 8;
         const int lane = threadIdx.x & 31, T = p.tile_tokens;
+        const bool few = p.num_seqs <= FEW;
         int64_t cost[PER], total = 0, mine = 0;
+        const ChunkSeq own = chunk_seq(p, min(lane, p.num_seqs - 1));  // few: sequence `lane`
+        auto seq_of = [&](int b) {
+            return ChunkSeq{__shfl_sync(0xffffffffu, own.q0, b), __shfl_sync(0xffffffffu, own.n, b),
+                            __shfl_sync(0xffffffffu, own.kv, b)};
+        };
         auto costs = [&](int base) {
             mine = 0;
             ChunkSeq q[PER];
@@ -84,28 +100,59 @@ struct KeyTileWalk {
                 mine += cost[i];
             }
         };
-        for (int base = 0; base < p.num_seqs; base += 32 * PER) {
-            costs(base);
-            total += warp_sum64(mine);
+        if (few) {  // mine: cost of a key head of sequence `lane`
+            for (int b = 0; b < p.num_seqs; ++b) {
+                const ChunkSeq s = seq_of(b);
+                const int tiles = (s.n + T - 1) / T;
+                int64_t sum = 0;
+                if (s.n > 0)
+                    for (int j = lane; j * KEYS < s.kv; j += 32) sum += item_cost(s, T, tiles, j);
+                sum = warp_sum64(sum);
+                total += sum * p.Hkv;
+                if (lane == b) mine = sum;
+            }
+        } else {
+            for (int base = 0; base < p.num_seqs; base += 32 * PER) {
+                costs(base);
+                total += warp_sum64(mine);
+            }
         }
         if (cta == 0)
             for (int b = lane; b < p.num_seqs; b += 32) chunk_check(p, b);
         int64_t per = div_up_or_down(total, ctas, true);
         if (per < KT) per = KT;  // at least a step
-        const int64_t start = per * cta;
+        const int64_t start = per * cta, end = min(start + per, total);
         if (start >= total) {
             if (lane == 0) *out = ChunkStart{0, 0, 0, 0, 0, 0, per};
             return;
         }
         int64_t before = 0;
+        if (few) {
+            for (int b = 0; b < p.num_seqs; ++b) {
+                const int64_t one = __shfl_sync(0xffffffffu, mine, b);
+                if (start >= before + one * p.Hkv) {
+                    before += one * p.Hkv;
+                    continue;
+                }
+                const ChunkSeq s = seq_of(b);
+                const int tiles = (s.n + T - 1) / T;
+                const int64_t h = div_up_or_down(start - before, one, false);
+                int64_t pos = before + h * one;
+                for (int j0 = 0; j0 * KEYS < s.kv; j0 += 32) {
+                    const int j = j0 + lane;
+                    const int64_t c = j * KEYS < s.kv ? item_cost(s, T, tiles, j) : 0;
+                    const int64_t incl = warp_scan64(c, lane), at = pos + incl - c;
+                    if (start >= at && start < at + c) *out = ChunkStart{b, static_cast<int>(h), j, at, start, end, per};
+                    pos += __shfl_sync(0xffffffffu, incl, 31);
+                    if (start < pos) break;
+                }
+                break;
+            }
+            return;
+        }
         for (int base = 0; base < p.num_seqs; base += 32 * PER) {
             if (p.num_seqs > 32 * PER) costs(base);
-            int64_t incl = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
+            const int64_t incl = warp_scan64(mine, lane);
             int64_t at = before + incl - mine;
             if (start >= at && start < at + mine) {
                 int b = base + lane * PER;
@@ -128,7 +175,7 @@ struct KeyTileWalk {
                     if (start < pos + n) break;
                     pos += n;
                 }
-                *out = ChunkStart{b, static_cast<int>(h), j, pos, start, min(start + per, total), per};
+                *out = ChunkStart{b, static_cast<int>(h), j, pos, start, end, per};
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
@@ -183,7 +230,7 @@ __global__ void __launch_bounds__(KtCfg<D>::THREADS, 1)
 key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const ChunkParams p) {
     using C = KtCfg<D>;
     using Walk = KeyTileWalk<C::KT, CAUSAL>;
-    constexpr int BN = C::BN, SW = C::SW, NQ = C::NQ, KT = C::KT, KB = C::KB;
+    constexpr int BN = C::BN, SW = C::SW, NQ = C::NQ, KT = C::KT, KB = C::KB, COLS = C::COLS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *sL = reinterpret_cast<float *>(smem + C::OFF_L);
@@ -211,7 +258,7 @@ key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         }
         for (int i = 0; i < 2 * KT; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&s_free[i], 4);
+            mbar_init(&s_free[i], 8);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -358,45 +405,36 @@ key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         }
     } else {
         // ------------------------------------------------------------ weights and their sums
-        const int a = warp >> 2, quarter = warp & 3;
-        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        const int a = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, in = a * BN + quarter * 32 + lane;
+        const uint32_t at_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + a * 2 * BN + half * COLS;
+        float *sums = reinterpret_cast<float *>(smem + C::OFF_SUM);
         const uint64_t c2 = f2(p.scale_log2, p.scale_log2);
         bool ok = true;
-        int u = 0, uses = 0;
+        int u = 0, uses = 0, it = 0;
         ChunkDesc desc{0, 0, 0, 0};
 #pragma unroll 1
-        for (bool more = w.begin(p, *start); more; more = w.next(p)) {
+        for (bool more = w.begin(p, *start); more; more = w.next(p), ++it) {
             if (w.t0 == w.first && w.t1 < w.first + w.steps) desc = w.desc(start->per);
             const bool mine = a == 0 || w.shift == 1;
-            const int key = w.j * C::KEYS + a * BN + quarter * 32 + lane;
+            const int key = w.j * C::KEYS + in;
             const bool busy = mine && key - lane < w.s.kv;  // this warp has a key
             float *at = p.weights + (static_cast<int64_t>(w.b) * p.Hkv + w.h) * p.width + key;
             const bool whole = w.whole();
-            const float was = whole && busy && key < w.s.kv ? *at : 0.f;
+            const float was = half == 0 && whole && busy && key < w.s.kv ? *at : 0.f;
             // tokens from `sees` on see this key
             const int sees = CAUSAL ? max(0, key - (w.s.kv - w.s.n)) : 0;
             uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll 1
             for (int t = w.t0; ok && t < w.t1; ++t, ++u) {
                 const int st = u % NQ;
-                uint32_t sr[BN];
+                const int buf = uses & 1;
                 if (mine) {
-                    const int buf = uses & 1;
                     if (!__all_sync(0xffffffffu, wait_bounded(&s_full[a * 2 + buf], (uses >> 1) & 1, abort_flag, lim, 797))) {
                         ok = false;
                         break;
                     }
                     ++uses;
                     tc_fence_after_sync();
-                    if (busy) {
-#pragma unroll
-                        for (int cc = 0; cc < BN / 32; ++cc) tmem_ld32(tmem + lane_base + (a * 2 + buf) * BN + cc * 32, sr + cc * 32);
-                        tmem_ld_wait();
-                        tmem_reg_fence<BN>(sr);
-                        tc_fence_before_sync();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_free[a * 2 + buf]);
                 }
                 // (every warp: an idle one that did not wait would release the stage rounds ahead)
                 if (!__all_sync(0xffffffffu, wait_bounded(&l_full[st], (u / NQ) & 1, abort_flag, lim, 798))) {
@@ -405,33 +443,48 @@ key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 }
                 if (busy) {
                     // columns [lo, hi) are rows that see the key
-                    const int lo = (sees - t * T) * p.G, hi = min(T, w.s.n - t * T) * p.G;
-                    if (__any_sync(0xffffffffu, lo > 0) || hi < BN) {
+                    const int lo = (sees - t * T) * p.G - half * COLS, hi = min(T, w.s.n - t * T) * p.G - half * COLS;
+                    const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < COLS;
 #pragma unroll
-                        for (int i = 0; i < BN; ++i)
-                            if (i < lo || i >= hi) sr[i] = __float_as_uint(-INFINITY);
-                    }
-                    const float4 *nl = reinterpret_cast<const float4 *>(sL + st * BN);
+                    for (int c = 0; c < COLS; c += 32) {  // 32 columns in registers at a time
+                        uint32_t sr[32];
+                        tmem_ld32(at_tmem + buf * BN + c, sr);
+                        tmem_ld_wait();
+                        tmem_reg_fence<32>(sr);
+                        if (masked) {
 #pragma unroll
-                    for (int i = 0; i < BN / 4; ++i) {
-                        const float4 l = nl[i];
-                        float x0, x1, x2, x3;
-                        f2_split(ffma2(f2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1])), c2, f2(l.x, l.y)), x0, x1);
-                        f2_split(ffma2(f2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3])), c2, f2(l.z, l.w)), x2, x3);
-                        acc[(2 * i) & 3] = fadd2(acc[(2 * i) & 3], f2(ex2_approx(x0), ex2_approx(x1)));
-                        acc[(2 * i + 1) & 3] = fadd2(acc[(2 * i + 1) & 3], f2(ex2_approx(x2), ex2_approx(x3)));
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < lo || c + i >= hi) sr[i] = __float_as_uint(-INFINITY);
+                        }
+                        const float4 *nl = reinterpret_cast<const float4 *>(sL + st * BN + half * COLS + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 l = nl[i];
+                            float x0, x1, x2, x3;
+                            f2_split(ffma2(f2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1])), c2, f2(l.x, l.y)), x0, x1);
+                            f2_split(ffma2(f2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3])), c2, f2(l.z, l.w)), x2, x3);
+                            acc[(2 * i) & 3] = fadd2(acc[(2 * i) & 3], f2(ex2_approx(x0), ex2_approx(x1)));
+                            acc[(2 * i + 1) & 3] = fadd2(acc[(2 * i + 1) & 3], f2(ex2_approx(x2), ex2_approx(x3)));
+                        }
                     }
+                    tc_fence_before_sync();
                 }
                 __syncwarp();
+                if (mine && lane == 0) mbar_arrive(&s_free[a * 2 + buf]);
                 if (lane == 0) mbar_arrive(&q_empty[st]);
             }
-            if (!ok || !busy) continue;
             float lo, hi;
             f2_split(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), lo, hi);
+            // the halves' sums, the items by turns (every warp takes every item, whatever became of its waits)
+            float *other = sums + (it & 1) * C::KEYS + in;
+            if (half == 1) *other = lo + hi;
+            asm volatile("bar.sync %0, 256;" ::"r"(1 + a) : "memory");
+            if (half == 1 || !ok || !busy) continue;
+            const float sum = (lo + hi) + *other;
             if (!whole)
-                p.part_o[static_cast<int64_t>(w.slot()) * C::KEYS + a * BN + quarter * 32 + lane] = lo + hi;
+                p.part_o[static_cast<int64_t>(w.slot()) * C::KEYS + in] = sum;
             else if (key < w.s.kv)
-                *at = was + (lo + hi);
+                *at = was + sum;
         }
         if (threadIdx.x == 0) p.desc[blockIdx.x] = desc;
     }
