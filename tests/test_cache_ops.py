@@ -652,6 +652,15 @@ def test_max_q_len_does_not_change_the_result(cuda_device, new, kv, max_q):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256, 512, 1024])
+def test_every_page_size(cuda_device, page, D, few):
+    new, kv = ([1, 2, 1], [5, 700, 257]) if few else ([30, 1, 17], [35, 700, 257])
+    check_chunk_and_weights(cuda_device, new, kv, 4, 2, D, page, "bf16", 7)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D,hq,hk", [(64, 128, 1), (32, 20, 1), (128, 34, 2), (256, 96, 3)])
 def test_many_heads_a_key_head(cuda_device, D, hq, hk):
     check_chunk_and_weights(cuda_device, [1, 3, 0, 9], [200, 3, 50, 300], hq, hk, D, 32, "fp16", 51)

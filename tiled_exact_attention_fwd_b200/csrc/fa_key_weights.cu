@@ -145,6 +145,8 @@ struct KeyWalk {
     }
 };
 
+constexpr int kKeyBox = 128;  // cache rows of a TMA box, at most (fa_key_weights_tile.cu's too)
+
 template <int D>
 struct KeyCfg {
     static constexpr int R = 16;                   // rows a step
@@ -192,7 +194,7 @@ key_weights_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const ChunkPar
         bool bad = false;
         int u = 0;
         const uint64_t pol = l2_policy_evict_first();
-        const int box = min(1 << p.page_shift, BN);
+        const int box = min(1 << p.page_shift, kKeyBox);
         for (bool more = w.begin(p, st); more; more = w.next(p), ++u) {
             const int stage = u % NS;
             if (u >= NS && !__all_sync(0xffffffffu, wait_bounded(&empty[stage], ((u / NS) - 1) & 1, abort_flag, p.timeout_ns, 730)))
@@ -350,7 +352,7 @@ cudaError_t launch_key_weights(int D, bool bf16, bool causal, const CUtensorMap 
     }
 }
 
-int key_weights_box(int page_size) { return page_size < 128 ? page_size : 128; }
+int key_weights_box(int page_size) { return page_size < kKeyBox ? page_size : kKeyBox; }
 
 cudaError_t key_weights_error_addrs(int **code, int **where) { return device_error_addrs(code, where); }
 
