@@ -42,11 +42,14 @@ struct KeyWalk {
     int64_t left;  // row tiles of the run that are left
     __device__ static int64_t head_cost(const ChunkParams &p, const ChunkSeq &s) {
         if (s.n == 0) return 0;
-        const int tiles = (s.n * p.G + R - 1) / R, jn = (s.kv + BN - 1) / BN;
-        if (!CAUSAL) return static_cast<int64_t>(tiles) * jn;
-        int64_t sum = 0;
-        for (int j = 0; j < jn; ++j) sum += tiles - first_tile<R, BN, CAUSAL>(p, s, j);
+        const int tiles = (s.n * p.G + R - 1) / R, jn = (s.kv + BN - 1) / BN, same = seen_by_all(s, jn);
+        int64_t sum = static_cast<int64_t>(tiles) * same;
+        for (int j = same; j < jn; ++j) sum += tiles - first_tile<R, BN, CAUSAL>(p, s, j);
         return sum;
+    }
+    // Key tiles that every row tile sees: the first so many of the sequence's jn.
+    __device__ static __forceinline__ int seen_by_all(const ChunkSeq &s, int jn) {
+        return !CAUSAL ? jn : (s.kv >= s.n ? min(jn, (s.kv - s.n) / BN + 1) : 0);
     }
     __device__ __forceinline__ void seq(const ChunkParams &p) {
         s = chunk_seq(p, b);
@@ -73,7 +76,7 @@ struct KeyWalk {
         }
         if (cta == 0)
             for (int b = lane; b < p.num_seqs; b += 32) chunk_check(p, b);
-        const int64_t per = (total + ctas - 1) / ctas, start = per * cta;
+        const int64_t per = div_up_or_down(total, ctas, true), start = per * cta;
         if (lane == 0) *st = KeyStart{0, 0, 0, 0};
         __syncwarp();
         if (start >= total) return;
@@ -95,12 +98,13 @@ struct KeyWalk {
                         const ChunkSeq s = chunk_seq(p, b);
                         const int tiles = (s.n * p.G + R - 1) / R;
                         int64_t rem = start - at;
-                        const int64_t one = cost[i] / p.Hkv;
-                        int h = static_cast<int>(rem / one);
+                        const int64_t one = div_up_or_down(cost[i], p.Hkv, false);
+                        int h = static_cast<int>(div_up_or_down(rem, one, false));
                         rem -= h * one;
                         // the first item whose own start lies at or after `start`
-                        int j = 0;
-                        int64_t sum = 0;
+                        int j = static_cast<int>(min(static_cast<int64_t>(seen_by_all(s, (s.kv + BN - 1) / BN)),
+                                                     div_up_or_down(rem, tiles, true)));
+                        int64_t sum = static_cast<int64_t>(j) * tiles;
                         while (sum < rem) {
                             sum += tiles - first_tile<R, BN, CAUSAL>(p, s, j);
                             ++j;

@@ -72,9 +72,15 @@ struct KeyTileWalk {
     __device__ static int64_t head_cost(const ChunkSeq &s, int T) {
         if (s.n == 0) return 0;
         const int tiles = (s.n + T - 1) / T;
-        int64_t sum = 0;
-        for (int j = 0; j * KEYS < s.kv; ++j) sum += item_cost(s, T, tiles, j);
+        int j = alike(s);
+        int64_t sum = static_cast<int64_t>(j) * (tiles * KT);
+        for (; j * KEYS < s.kv; ++j) sum += item_cost(s, T, tiles, j);
         return sum;
+    }
+    // The first so many items cost the same: every row tile sees them, and they have KT key tiles.
+    __device__ static __forceinline__ int alike(const ChunkSeq &s) {
+        const int full = (s.kv - 1) / KEYS;  // (all but the last)
+        return !CAUSAL ? full : (s.kv >= s.n ? min(full, (s.kv - s.n) / KEYS + 1) : 0);
     }
     // As chunk_locate: a few sequences one by one, a lane per item; many with four per lane. (A lane a sequence took
     // 6 us for two of 52 items.)
@@ -169,7 +175,8 @@ struct KeyTileWalk {
                 const int64_t one = div_up_or_down(mine_b, p.Hkv, false);
                 const int64_t h = div_up_or_down(start - at, one, false);
                 int64_t pos = at + h * one;
-                int j = 0;
+                int j = static_cast<int>(min(static_cast<int64_t>(alike(s)), div_up_or_down(start - pos, tiles * KT, false)));
+                pos += static_cast<int64_t>(j) * (tiles * KT);
                 for (;; ++j) {
                     const int64_t n = item_cost(s, T, tiles, j);
                     if (start < pos + n) break;
