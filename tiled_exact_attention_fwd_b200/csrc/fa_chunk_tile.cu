@@ -18,6 +18,11 @@
 //   warp 11         Q tiles by TMA, each once the last item's QKs have read its buffer.
 // Rows of a tile past the sequence's last are computed on whatever lies there and not stored; a
 // softmax warp without a row skips the exponentials. An item that the split cuts leaves O, m and l in the workspace.
+//
+// Bound, as the dense forward, by softmax and MMAs waiting for one another (both pipes 54 % busy); measured with
+// the joining: 2048 tokens over 8192 keys (32 heads on 8, D = 128) 220 us, 1.09 PFLOP/s (fa_fwd on a problem of
+// the same products 1.16); 9 sequences of up to 333 tokens over 2777 (D = 64) 51 us, where starting and joining
+// are a third.
 #include "fa_chunk.cuh"
 #include "fa_fwd_kernel.cuh"
 
