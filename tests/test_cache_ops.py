@@ -241,6 +241,10 @@ NORM = [  # tokens, hq, hk, D, rot, dtype, weights, interleaved, fused
     (13, 6, 3, 256, 256, "bf16", "fp32", False, False),
     (9, 2, 1, 256, 64, "fp16", "same", True, True),
     (700, 12, 4, 64, 64, "bf16", "same", False, False),
+    # more batches than warps, a part of a batch at the end of each token
+    (6001, 5, 1, 32, 32, "bf16", "same", False, False),
+    (1501, 17, 3, 128, 64, "fp16", "fp32", True, True),
+    (2100, 1, 9, 256, 256, "bf16", "same", False, False),
 ]
 
 

@@ -134,7 +134,6 @@ struct QkNormParams {
     const int32_t *cu_seqlens, *kv_lens, *block_table;
     int num_seqs, max_blocks, page_shift, num_pages;
     // set by the launcher
-    int heads_per_warp, q_units, k_units;       // heads of a work unit, units a token
     int ctas_q, ctas_k;                         // CTAs of the q rows, of the k rows (and again of the v rows)
 };
 constexpr int kQkNormCtas = 296;                // most of a launch (two an SM), give or take one

@@ -13,7 +13,7 @@
 // written). A lane takes two 16-byte chunks of a row, chosen so that both halves of each pair are
 // its own (Turn): no exchange but the row's sum, log2(D / 16) shuffles, and all arithmetic in pairs of
 // floats (with a chunk a lane, and the partners' values by shuffles, the instructions took as long as the
-// bytes). Two CTAs an SM walk over the tokens, each warp with the rows of three batches in flight while it
+// bytes). Two CTAs an SM walk over the tokens, each warp with the rows of two batches in flight while it
 // works on one. All arithmetic is 32-bit; an output is rounded once. The weight gradients are summed in
 // registers, then over the CTA's warps in shared memory, then over the CTAs by a second launch in a
 // fixed order (no atomics: the same inputs give the same bits).
@@ -22,6 +22,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "fa.h"
 #include "fa_internal.h"
@@ -244,45 +246,45 @@ struct Share {
     }
 };
 
-// A warp's walk over the work units of its kind: a unit is one token and up to p.heads_per_warp
-// consecutive heads, worked on in batches of `batch` heads.
+// A warp's walk over the rows of its kind: batches of `batch` heads of a token, an equal run of neighbouring ones
+// for each warp (so that the tokens need not divide by the warps, and a run's batches share their token's
+// angles).
 struct Walk {
-    int64_t unit, units, step, tok;
-    int per_token, heads, per_unit, hb, h1;
-    __device__ __forceinline__ Walk(const QkNormParams &p, const Share &sh) {
-        per_token = sh.kind == 0 ? p.q_units : p.k_units;
+    int64_t tok, left, last;
+    int heads, batch, hb;
+    __device__ __forceinline__ Walk(const QkNormParams &p, const Share &sh, int batch_) : last(p.n - 1), batch(batch_) {
         heads = sh.kind == 0 ? p.Hq : p.Hk;
-        per_unit = p.heads_per_warp;
-        units = p.n * per_token;
-        step = static_cast<int64_t>(sh.ctas) * kWarps;
-        unit = static_cast<int64_t>(sh.cta) * kWarps + (threadIdx.x >> 5);
-        enter();
+        const int per = (heads + batch - 1) / batch;
+        const int64_t total = p.n * per, warps = static_cast<int64_t>(sh.ctas) * kWarps;
+        const int64_t w = static_cast<int64_t>(sh.cta) * kWarps + (threadIdx.x >> 5);
+        const int64_t whole = total / warps, rest = total - whole * warps, first = whole * w + (w < rest ? w : rest);
+        left = whole + (w < rest ? 1 : 0);
+        tok = first / per;
+        hb = static_cast<int>(first - tok * per) * batch;
     }
-    __device__ __forceinline__ bool more() const { return unit < units; }
-    __device__ __forceinline__ void enter() {
-        tok = unit / per_token;
-        hb = static_cast<int>(unit - tok * per_token) * per_unit;
-        h1 = min(heads, hb + per_unit);
-    }
-    // to the next batch; true where it begins a unit
-    __device__ __forceinline__ bool next(int batch) {
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    // to the next batch; true where it begins a token
+    __device__ __forceinline__ bool next() {
+        --left;
         hb += batch;
-        if (hb < h1) return false;
-        unit += step;
-        enter();
+        if (hb < heads) return false;
+        hb = 0;
+        ++tok;
         return true;
     }
-    // token of the unit after this one (this one's where there is none)
-    __device__ __forceinline__ int64_t next_token() const { return unit + step < units ? (unit + step) / per_token : tok; }
+    // the token after this one (this one where there is none)
+    __device__ __forceinline__ int64_t next_token() const { return tok < last ? tok + 1 : last; }
 };
 
 // Measured at 8192 tokens of 64 heads of 128 (forward / backward, us): two rows a lane, two CTAs an SM and
-// four slots 50.6 / 77.5 (as fast as a plain copy of the forward's bytes, 51); three CTAs, whose registers
-// spill, 54.5 / 105; one row and six slots 50.3 / 98; six slots 50.8 / 79; the next rows in registers
-// instead of a ring 60.5 / 86.
+// three slots 51 / 72 (as fast as a plain copy of the forward's bytes, 51); four slots 53 / 71; two slots 53 / 91; four rows in the
+// backward 71.6. Three CTAs, whose registers spill, 54.5 / 105; the next rows in registers instead of a ring 60.5 / 86.
+// Runs of neighbouring batches for each warp, against whole tokens by turns: 32 heads beside 8 of 128 38 / 56 against 41 /
+// 60, beside 2 of 64 21 / 34 against 82 / 91 (there the CTAs were shared out by heads, and a token of few heads costs a
+// warp as much as one of many); 32 beside 32, where the tokens divide by the warps, 51 / 72 against 49 / 76.
 constexpr int kRows = 2;   // rows a lane takes at a time
 constexpr int kPerSm = 2;  // CTAs an SM
-constexpr int kSlots = 4;  // batches in the ring, one of them being worked on
+constexpr int kSlots = 3;  // batches in the ring, one of them being worked on
 
 // Rows on their way: each thread copies its own chunks into its own places of a ring of kSlots batches in
 // shared memory (cp.async) and reads them back itself, so nothing has to be synchronised, and what is in
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_fwd_kernel(const QkN
     const uint16_t *x0 = static_cast<const uint16_t *>(kind == 0 ? p.q : (kind == 1 ? p.k : p.v));
     const int64_t xs = kind == 0 ? p.q_stride : (kind == 1 ? p.k_stride : p.v_stride);
     bool bad = false, lost = false;
-    Walk w(p, sh);
+    Walk w(p, sh, BATCH);
     if (!w.more()) return;
     // where token w.tok's row of heads goes (PAGED: null where it has no place), and its position
     auto place = [&](int64_t &pos) -> uint16_t * {
@@ -349,12 +351,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_fwd_kernel(const QkN
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int h = wl.hb + i * RPI + row_in;
-                const bool there = h < wl.h1;
+                const bool there = h < wl.heads;
                 const uint16_t *x = x0 + wl.tok * xs + (there ? h * D : 0);
                 ring.put(2 * i, x + turn.A, there);
                 ring.put(2 * i + 1, x + turn.B, there);
             }
-            wl.next(BATCH);
+            wl.next();
         }
         ring.filled();
     };
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_fwd_kernel(const QkN
         for (int i = 0; i < U; ++i) {
             const int h = w.hb + i * RPI + row_in;
             uint16_t *out = dst + h * D;
-            const bool store = dst && h < w.h1;
+            const bool store = dst && h < w.heads;
             const uint4 va = ring.get(2 * i), vb = ring.get(2 * i + 1);
             if (PAGED && kind == 2) {  // values: a copy
                 if (store) {
@@ -409,8 +411,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_fwd_kernel(const QkN
         }
         ring.next();
         fetch();  // into the slot of the batch before
-        if (w.next(BATCH)) {
-            if (!w.more()) break;
+        const bool turned_to = w.next();
+        if (!w.more()) break;
+        if (turned_to) {
             pos = pos_next;
             dst = place(pos);
             if (kind < 2) {
@@ -440,19 +443,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_bwd_kernel(const QkN
     const int64_t xs = kind == 0 ? p.q_stride : p.k_stride, dys = kind == 0 ? p.dq_out_stride : p.dk_out_stride;
     const int64_t dxs = kind == 0 ? p.q_out_stride : p.k_out_stride;
     bool bad = false;
-    Walk w(p, sh), wl = w;  // wl: of the loads
+    Walk w(p, sh, BATCH), wl = w;  // wl: of the loads
     Ring<2 * U> ring(smem);
     auto fetch = [&]() {
         if (wl.more()) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 const int h = wl.hb + i * RPI + row_in;
-                const bool there = h < wl.h1;
+                const bool there = h < wl.heads;
                 const int at = there ? h * D : 0;
                 ring.put(2 * i, x0 + wl.tok * xs + at, there);
                 ring.put(2 * i + 1, dy0 + wl.tok * dys + at, there);
             }
-            wl.next(BATCH);
+            wl.next();
         }
         ring.filled();
     };
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_bwd_kernel(const QkN
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int h = w.hb + i * RPI + row_in;
-            const bool there = h < w.h1;
+            const bool there = h < w.heads;
             const uint4 vx = ring.get(2 * i), vy = ring.get(2 * i + 1);
             uint64_t x[4], g[4], o[4];
             unpack8<BF16>(vx, x);
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_bwd_kernel(const QkN
         }
         ring.next();
         fetch();  // into the slot of the batch before
-        if (w.next(BATCH) && w.more()) {
+        if (w.next() && w.more()) {
             turn.load(angle_row(p, pos_next, bad), p.rot);
             pos_next = p.positions[w.next_token()];
         }
@@ -589,26 +592,19 @@ cudaError_t launch_ring(int bytes, int grid, const QkNormParams &p, cudaStream_t
 
 template <int D, bool BF16, bool INTER>
 cudaError_t launch_d(bool backward, QkNormParams p, cudaStream_t st) {
-    const int batch = backward ? 32 / (D / 8) * kRows : 32 / (D / 16) * kRows;  // heads a warp works on at a time
+    const int batch = 32 / (backward ? D / 8 : D / 16) * kRows;  // heads a warp works on at a time
     const bool paged = p.cu_seqlens != nullptr;
-    // kPerSm CTAs an SM, shared out by the kinds' heads. A unit is one batch while that leaves CTAs idle, else
-    // up to four batches of a token, which share its angles.
-    const int most = kQkNormCtas;
-    auto units = [&](int heads, int per) { return static_cast<int64_t>((heads + per - 1) / per); };
-    const int heads = p.Hq + p.Hk * (paged ? 2 : 1);
-    p.heads_per_warp = batch;
-    if (p.n * (units(p.Hq, batch) + units(p.Hk, batch) * (paged ? 2 : 1)) > static_cast<int64_t>(most) * kWarps * 4)
-        p.heads_per_warp = 4 * batch;
-    p.q_units = static_cast<int>(units(p.Hq, p.heads_per_warp));
-    p.k_units = static_cast<int>(units(p.Hk, p.heads_per_warp));
-    auto share = [&](int of_heads, int per_token) {
-        const int64_t need = (p.n * per_token + kWarps - 1) / kWarps;
-        int64_t mine = static_cast<int64_t>(most) * of_heads / heads;
-        if (mine < 1) mine = 1;
-        return static_cast<int>(need < mine ? need : mine);
+    // kPerSm CTAs an SM, shared out by the kinds' rows as they are worked on (whole batches), no more than there are
+    // batches for.
+    const int64_t most = kQkNormCtas;
+    auto batches = [&](int heads) { return static_cast<int64_t>((heads + batch - 1) / batch); };
+    const int64_t all = batches(p.Hq) + batches(p.Hk) * (paged ? 2 : 1);
+    auto share = [&](int heads) {
+        const int64_t need = (p.n * batches(heads) + kWarps - 1) / kWarps, mine = most * batches(heads) / all;
+        return static_cast<int>(std::min(need, std::max<int64_t>(mine, 1)));
     };
-    p.ctas_q = share(p.Hq, p.q_units);
-    p.ctas_k = share(p.Hk, p.k_units);
+    p.ctas_q = share(p.Hq);
+    p.ctas_k = share(p.Hk);
     const int grid = p.ctas_q + p.ctas_k + (paged ? p.ctas_k : 0);
     if (backward) {
         cudaError_t e = launch_ring<qk_norm_bwd_kernel<D, BF16, INTER>>(Ring<2 * kRows>::BYTES, grid, p, st);
