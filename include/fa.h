@@ -320,8 +320,8 @@ FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const vo
  *                zero: all of them. A row that sees no key gets out = 0 and lse = -inf.
  *   max_q_len    the most new tokens of a sequence. It chooses the kernel and the workspace's size, not the
  *                result.
- *   out          (total, Hq, D); lse (Hq, total) float32 or NULL. Rows of no sequence are left as
- *                they are.
+ *   out          (total, Hq, D); lse (Hq, total) float32 or NULL; neither overlaps an input. Rows of no
+ *                sequence are left as they are.
  *   workspace    fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len) bytes, 256-byte aligned, contents
  *                of no matter. Calls that overlap on the GPU (other streams, graphs replayed at the same
  *                time) need one each.
