@@ -317,7 +317,8 @@ FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const vo
  *   kv_lens      device int32 [num_seqs]: keys of each sequence, the new tokens' own included, at most
  *                2^31 - 2^16. Sequences may share pages.
  *   causal       nonzero: new token i of n sees keys 0 .. kv_lens[b] - n + i (aligned at the end);
- *                zero: all of them. A row that sees no key gets out = 0 and lse = -inf.
+ *                zero: all of them. A row that sees no key (or none whose score is above -inf) gets out = 0
+ *                and lse = -inf, one that sees a score of NaN or +inf NaN in both.
  *   max_q_len    the most new tokens of a sequence. It chooses the kernel and the workspace's size, not the
  *                result.
  *   out          (total, Hq, D); lse (Hq, total) float32 or NULL; neither overlaps an input. Rows of no

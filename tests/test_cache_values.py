@@ -7,7 +7,24 @@ import torch
 
 import fa_inputs
 from oracle import cache as oc
-from test_cache_ops import DT, U, chunk_inputs, within
+from test_cache_ops import DT, U, chunk_inputs, half_step, score_tol, within
+
+
+def check(dev, q, kc, vc, bt, cu, lens, max_q, dt, causal=True, scale=None):
+    """Attention and key weights against their definitions (test_cache_ops.py derives the tolerances)."""
+    import tiled_exact_attention_fwd_b200 as fa
+    args = [t.to(dev) for t in (q, kc, vc, bt, cu, lens)]
+    out, lse = fa.fa_fwd_paged_chunk(*args, max_q, causal=causal, scale=scale)
+    ref, rl, size, ssize = oc.chunk_attention(q, kc, vc, bt, cu, lens, causal=causal, scale=scale)
+    e = score_tol(ssize)
+    w = torch.zeros(len(lens), kc.shape[2], bt.shape[1] * kc.shape[1], device=dev)
+    fa.fa_paged_key_weights(args[0], args[1], *args[3:], max_q, lse, w, causal=causal, scale=scale)
+    add, most = oc.key_weights(q, kc, bt, cu, lens, lse.cpu(), w.shape[2], causal=causal, scale=scale)
+    assert fa.fa_device_status()[0] == 0
+    within(out, ref, half_step(dt) * ref.abs() + (half_step(dt) + 2 * e.t()[..., None]) * size + 2.0 ** -25, "out")
+    within(lse, rl, e + 2.0 ** -23 * rl.abs(), "lse")
+    within(w, add, (2.0 ** -19 * (most + 1) + 1024 * U) * add, "weights")
+    return out, lse, w
 
 
 # Sequences, new tokens of each, keys of each. One sequence: each step (64 or 128 keys) is a run of its own, so every
@@ -40,3 +57,79 @@ def test_key_weights_of_rows_without_a_finite_lse(cuda_device, D, layout, few):
     assert bool(nan[:, 0, :seen].all()) and not bool(nan[:, 0, seen:].any()) and not bool(nan[:, 1].any())
     within(w, add, (2.0 ** -19 * (most + 1) + 1024 * U) * add, "weights")
     assert fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("layout", ["cut", "whole"])
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("where", ["query", "keys", "last key"])
+def test_nan_stays_nan(cuda_device, where, D, layout, few):
+    """NaN in one row of each sequence, in a run of keys of one key head (a whole step of the split), or in the
+    last key of one key head: NaN in every row that sees it and in the weights of the keys that such a row
+    sees, whether the split cuts its item or not, and in nothing else."""
+    count, kv = LAYOUTS[layout]
+    n = 1 if few else 20
+    dtype = "bf16" if D > 64 else "fp16"
+    q, kc, vc, bt, cu, lens = chunk_inputs([n] * count, [kv] * count, 4, 2, D, 16, dtype, 3 + D, behind=0)
+    if where == "query":
+        q[n // 2::n, 1] = math.nan
+    else:
+        first, end = {"keys": (128, 256) if layout == "cut" else (64, 128), "last key": (kv - 1, kv)}[where]
+        for b in range(count):
+            for i in range(first, end):
+                kc[bt[b, i // 16], i % 16, 1] = math.nan
+    out, lse, w = check(cuda_device, q, kc, vc, bt, cu, lens, n, DT[dtype])
+    rows = torch.isnan(lse.t()).cpu()  # (token, head)
+    want = torch.zeros_like(rows)
+    if where == "query":
+        want[n // 2::n, 1] = True
+    elif where == "keys":
+        want[:, 2:] = True
+    else:
+        want[n - 1::n, 2:] = True
+    assert torch.equal(rows, want) and torch.equal(torch.isnan(out).all(-1).cpu(), want) and torch.equal(torch.isnan(out).any(-1).cpu(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("few", [True, False])
+@pytest.mark.parametrize("layout", ["cut", "whole"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinite_scores(cuda_device, D, layout, few):
+    """One infinite value in a key: its score is +inf for some rows (NaN, as a softmax over it is) and -inf for the
+    others, for which the key is as if it were not there."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, dt = cuda_device, torch.bfloat16
+    count, kv = LAYOUTS[layout]
+    n, at = 1 if few else 20, 70
+    q, kc, vc, bt, cu, lens = chunk_inputs([n] * count, [kv] * count, 4, 2, D, 16, "bf16", 5 + D, behind=0)
+    for b in range(count):
+        kc[bt[b, at // 16], at % 16, :, 0] = math.inf
+    args = [t.to(dev) for t in (q, kc, vc, bt, cu, lens)]
+    out, lse = fa.fa_fwd_paged_chunk(*args, n)
+    ref, rl, size, _ = oc.chunk_attention(q, kc, vc, bt, cu, lens)
+    _, _, _, ssize = oc.chunk_attention(q, torch.where(kc.isinf(), torch.zeros_like(kc), kc), vc, bt, cu, lens)
+    up = (q[..., 0] > 0)  # (token, head): score +inf
+    assert bool((q[..., 0] != 0).all()) and bool((~up).any())  # (4 rows may all be of one sign)
+    assert torch.equal(torch.isnan(out).all(-1).cpu(), up) and torch.equal(torch.isnan(lse.t()).cpu(), up)
+    e = score_tol(ssize)
+    tol = half_step(dt) * ref.abs() + (half_step(dt) + 2 * e.t()[..., None]) * size
+    within(out.cpu()[~up], ref[~up], tol[~up], "out")
+    within(lse.t().cpu()[~up], rl.t()[~up], (e + 2.0 ** -23 * rl.abs()).t()[~up], "lse")
+    w = torch.zeros(count, 2, bt.shape[1] * 16, device=dev)
+    fa.fa_paged_key_weights(args[0], args[1], *args[3:], n, lse, w)
+    add, most = oc.key_weights(q, torch.where(kc.isinf(), torch.zeros_like(kc), kc), bt, cu, lens, lse.cpu(), w.shape[2])
+    add[..., at] = torch.where(torch.isnan(add[..., at]), add[..., at], torch.zeros(()).double())
+    within(w, add, (2.0 ** -19 * (most + 1) + 1024 * U) * add, "weights")
+    assert fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [[1, 1], [20, 3]])
+def test_infinite_values(cuda_device, new):
+    """An infinite value in a column of V that every row sees: that column is infinite, the others as they are."""
+    q, kc, vc, bt, cu, lens = chunk_inputs(new, [300, 40], 4, 2, 64, 16, "bf16", 8, behind=0)
+    for b in range(2):
+        vc[bt[b, 0], 5, 1, 7] = math.inf
+    out, _, _ = check(cuda_device, q, kc, vc, bt, cu, lens, max(new), torch.bfloat16)
+    assert bool((out[:, 2:, 7] == math.inf).all()) and int(torch.isinf(out).sum()) == 2 * sum(new)

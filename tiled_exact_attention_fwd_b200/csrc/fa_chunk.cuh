@@ -354,7 +354,8 @@ __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepc
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Joins the pieces of the item that CTA blockIdx.x began and did not finish: m = max of the pieces', l
-// and O summed with each piece scaled by 2^(m_i - m), the maximum running as in the attention itself. A lane
+// and O summed with each piece scaled by 2^(m_i - m), the maximum running as in the attention itself; NaN in a
+// piece's l or O stays NaN. A lane
 // takes four neighbouring rows (one 16-byte load of a column), a warp LR * 4 rows and CL columns at a load;
 // the loads of several pieces are issued together, before anything is known of the pieces (what the joining
 // takes is latency: one load after another, it took 6 us for four pieces of 16 rows and 20 us for two of
@@ -408,8 +409,9 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p)
         for (int q = 0; q < C::AHEAD; ++q)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // a piece in which the row saw nothing (or that was read twice) adds nothing
-                if (k + q >= d.pieces || pm[q][i] == -INFINITY) continue;
+                // a piece in which the row saw nothing (l = 0), or that was read twice, adds nothing. (Its m does not
+                // say so: the maximum passes over NaN, and a piece of NaN scores alone has m = -inf beside l = NaN.)
+                if (k + q >= d.pieces || pl[q][i] == 0.f) continue;
                 const float to = fmaxf(m[i], pm[q][i]);
                 const float a0 = ex2_approx(m[i] - to), a1 = ex2_approx(pm[q][i] - to);  // (2^-inf = 0 at the first)
                 m[i] = to;
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p)
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + i, sub = r / half, rr = r - sub * half, ti = rr / p.G, tk = sub * T + ti;
         if (ti >= T || tk >= d.tokens) continue;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
         const int64_t tok = d.token + tk;
         const int head = d.head + rr - ti * p.G;
         uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D + c0;
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const ChunkParams p)
             }
         }
         if (p.lse && c0 == 0)
-            p.lse[static_cast<int64_t>(head) * p.total + tok] = l[i] > 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
+            p.lse[static_cast<int64_t>(head) * p.total + tok] = l[i] == 0.f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
     }
 }
 

@@ -297,7 +297,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     }
                     const int64_t tok = w.s.q0 + w.i0 + row / p.G;
                     const int head = w.h * p.G + row % p.G;
-                    const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                     uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D + half * C::DH;
                     const int64_t slot = w.slot();
                     float *po = p.part_o + (slot * D + half * C::DH) * R + row;
@@ -329,7 +329,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                             p.part_ml[slot * R + row] = make_float2(m, l);
                         else if (p.lse)
                             p.lse[static_cast<int64_t>(head) * p.total + tok] =
-                                l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+                                l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
                     }
                 }
                 consumers_sync<32 * C::NW>();

@@ -484,7 +484,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             const int ti = r / p.G;
             const int64_t tok = w.s.q0 + w.i0 + first + ti;
             const int head = w.h * p.G + r - ti * p.G;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             uint16_t *out = static_cast<uint16_t *>(p.out) + (tok * p.Hq + head) * D;
             const int64_t slot = w.slot();
             const int pr = split ? r : t * BM + r;              // row of the item's tile
@@ -530,7 +530,7 @@ chunk_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             if (!whole)
                 p.part_ml[slot * C::R + pr] = make_float2(m, l);
             else if (row_ok && p.lse)
-                p.lse[static_cast<int64_t>(head) * p.total + tok] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+                p.lse[static_cast<int64_t>(head) * p.total + tok] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
         }
     }
     tc_fence_before_sync();
