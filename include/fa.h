@@ -288,8 +288,8 @@ FA_API fa_status fa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void
  *                goes to slot kv_lens[b] - n + i. A slot outside the table or a table entry
  *                outside the pool: that token's k and v are not written and FA_ERR_INDEX is left for
  *                fa_device_status.
- *   positions    device int64 [n] as above, or NULL: each token's slot is its position (they differ once
- *                keys have been evicted).
+ *   positions    device int64 [n] as above (of rows of no sequence: anything), or NULL: each token's slot is its
+ *                position (they differ once keys have been evicted).
  *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
  *                of (page_size, Hkv, D).
  * The rest as fa_qk_norm_rope.

@@ -7,7 +7,7 @@ import torch
 
 import fa_inputs
 from oracle import cache as oc
-from test_cache_ops import DT, U, chunk_inputs, half_step, score_tol, within
+from test_cache_ops import DT, U, chunk_inputs, half_step, norm_inputs, on, pools, round_tol, score_tol, within
 
 
 def check(dev, q, kc, vc, bt, cu, lens, max_q, dt, causal=True, scale=None):
@@ -133,3 +133,32 @@ def test_infinite_values(cuda_device, new):
         vc[bt[b, 0], 5, 1, 7] = math.inf
     out, _, _ = check(cuda_device, q, kc, vc, bt, cu, lens, max(new), torch.bfloat16)
     assert bool((out[:, 2:, 7] == math.inf).all()) and int(torch.isinf(out).sum()) == 2 * sum(new)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hk,D,behind", [(4, 2, 64, 3), (3, 1, 256, 40), (32, 8, 128, 700)])
+def test_append_with_rows_of_no_sequence(cuda_device, hq, hk, D, behind):
+    """Rows behind the last sequence may hold any position: nothing of theirs is written or reported; a token of a
+    sequence whose position is outside the table still is."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, new, kv, page = cuda_device, [3, 0, 1, 5], [20, 7, 1, 64], 16
+    total = sum(new)
+    q, k, v, wq, wk, cs, pos = norm_inputs(total + behind, hq, hk, D, D, torch.bfloat16, torch.bfloat16, True, 9)
+    pos[total:] = torch.tensor([-1, 1 << 40, 97, -(1 << 62)]).repeat(behind)[:behind]
+    _, _, bt = pools(kv, page, hk, D, torch.bfloat16, 6)
+    kc, vc = (torch.full((sum(-(-n // page) for n in kv) + 2, page, hk, D), 3.0, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    cu = fa_inputs.cu_seqlens_from_lengths(new)
+    lens = torch.tensor(kv, dtype=torch.int32)
+    for bad in (False, True):
+        if bad:
+            pos[total - 1] = 97
+        out = torch.full((total + behind, hq, D), 7.0, dtype=torch.bfloat16, device=dev)
+        fa.fa_qk_norm_rope_paged(on(dev, q), on(dev, k), on(dev, v), wq.to(dev), wk.to(dev), cs.to(dev), pos.to(dev), kc, vc,
+                                 bt.to(dev), cu.to(dev), lens.to(dev), q_out=out)
+        assert fa.fa_device_status()[0] == (-8 if bad else 0)
+        live = total - int(bad)
+        ref, size = oc.norm_rope(q[:live], wq, cs, pos[:live], 1e-6, False)
+        within(out[:live], ref, round_tol(ref, size, torch.bfloat16, 32), "q")
+        assert bool((out[total:] == 7.0).all())
+        for pool in (kc, vc):
+            assert int((pool != 3.0).any(-1).any(-1).sum()) == total  # the tokens' rows, and no others

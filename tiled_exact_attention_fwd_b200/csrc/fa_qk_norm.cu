@@ -325,10 +325,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_norm_fwd_kernel(const QkN
         if constexpr (!PAGED) {
             return static_cast<uint16_t *>(kind == 0 ? p.q_out : p.k_out) + w.tok * (kind == 0 ? p.q_out_stride : p.k_out_stride);
         } else {
-            // rows of no sequence stay as they are
-            if (w.tok < p.cu_seqlens[0] || w.tok >= p.cu_seqlens[p.num_seqs]) return nullptr;
-            const int b = warp_seq_of_token(p.cu_seqlens, p.num_seqs, static_cast<int>(w.tok), lane);
-            if (b < 0 || b >= p.num_seqs) return nullptr;  // offsets that do not rise
+            // rows of no sequence stay as they are, and what their positions hold does not matter (a batch of a fixed
+            // size leaves old or negative ones there)
+            const bool in = w.tok >= p.cu_seqlens[0] && w.tok < p.cu_seqlens[p.num_seqs];
+            const int b = in ? warp_seq_of_token(p.cu_seqlens, p.num_seqs, static_cast<int>(w.tok), lane) : -1;
+            if (b < 0 || b >= p.num_seqs) {  // (or offsets that do not rise)
+                pos = 0;
+                return nullptr;
+            }
             const int64_t slot = static_cast<int64_t>(p.kv_lens[b]) - p.cu_seqlens[b + 1] + w.tok;
             if (!p.positions) pos = slot;
             if (kind == 0) return static_cast<uint16_t *>(p.q_out) + w.tok * p.q_out_stride;
