@@ -321,8 +321,8 @@ FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const vo
  *                and lse = -inf, one that sees a score of NaN or +inf NaN in both.
  *   max_q_len    the most new tokens of a sequence. It chooses the kernel and the workspace's size, not the
  *                result.
- *   out          (total, Hq, D); lse (Hq, total) float32 or NULL; neither overlaps an input. Rows of no
- *                sequence are left as they are.
+ *   out          (total, Hq, D); lse (Hq, total) float32 or NULL. Rows of no sequence are left as they
+ *                are. Neither they nor the workspace overlap an input or one another (FA_ERR_SHAPE).
  *   workspace    fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len) bytes, 256-byte aligned, contents
  *                of no matter. Calls that overlap on the GPU (other streams, graphs replayed at the same
  *                time) need one each.
@@ -346,7 +346,8 @@ FA_API fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const vo
  *   lse          (Hq, total) float32 that fa_fwd_paged_chunk returned for the same arguments (-inf
  *                rows give nothing).
  *   weights      float32 (num_seqs, Hkv, width), width >= max_blocks_per_seq * page_size; slots at and
- *                past kv_lens[b] are not touched. Each sum is formed in a fixed order.
+ *                past kv_lens[b] are not touched. Each sum is formed in a fixed order. Neither they nor
+ *                the workspace overlap another argument (FA_ERR_SHAPE).
  *   workspace    fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len) bytes, 256-byte aligned, contents of
  *                no matter (0 bytes where a key head has at most 16 rows: NULL will do).
  * Calls that overlap on the GPU must share neither `weights` nor the workspace.

@@ -1,0 +1,48 @@
+"""Calls of the operators around a paged cache whose results overlap what they read or one another: refused on
+the host. No GPU is needed: no address here is ever read."""
+import pytest
+
+MB = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from tiled_exact_attention_fwd_b200 import build
+    build.build()
+    import tiled_exact_attention_fwd_b200 as fa
+    return fa.lib()
+
+
+class TestChunk:
+    """q and out: 4 * 4 * 64 * 2 = 2048 bytes, lse 64, pools 9 * 16 * 2 * 64 * 2 = 36864, table 32, cu_seqlens 12,
+    kv_lens 8."""
+
+    def call(self, lib, **kw):
+        a = dict(q=MB, kc=2 * MB, vc=3 * MB, bt=4 * MB, mb=4, page=16, pages=9, cu=5 * MB, kv=6 * MB, num=2, total=4, mq=2,
+                 out=7 * MB, lse=8 * MB, ws=16 * MB, wsb=1 << 40, hq=4, hk=2, d=64, scale=0.0, causal=1, dt=0)
+        a.update(kw)
+        return lib.fa_fwd_paged_chunk(*a.values(), None)
+
+    @pytest.mark.parametrize("change", [
+        dict(out=MB), dict(out=MB + 2032), dict(out=MB - 2032), dict(out=2 * MB + 36848), dict(out=3 * MB), dict(out=4 * MB - 2032),
+        dict(out=4 * MB + 16), dict(out=5 * MB), dict(out=6 * MB), dict(lse=MB), dict(lse=2 * MB - 60), dict(lse=4 * MB + 28),
+        dict(lse=5 * MB + 8), dict(lse=6 * MB - 60), dict(lse=7 * MB + 2044), dict(lse=7 * MB - 60), dict(out=16 * MB), dict(lse=16 * MB + 4),
+        dict(ws=7 * MB), dict(ws=2 * MB), dict(ws=MB), dict(ws=MB // 2, mq=9, q=MB)])
+    def test_overlaps(self, lib, change):
+        assert self.call(lib, **change) == -2
+
+
+class TestKeyWeights:
+    """weights: 2 * 2 * 64 * 4 = 1024 bytes."""
+
+    def call(self, lib, **kw):
+        a = dict(q=MB, kc=2 * MB, bt=4 * MB, mb=4, page=16, pages=9, cu=5 * MB, kv=6 * MB, num=2, total=4, mq=2, lse=7 * MB,
+                 w=8 * MB, width=64, ws=16 * MB, wsb=1 << 30, hq=4, hk=2, d=64, scale=0.0, causal=1, dt=0)
+        a.update(kw)
+        return lib.fa_paged_key_weights(*a.values(), None)
+
+    @pytest.mark.parametrize("change", [
+        dict(w=MB), dict(w=MB - 1020), dict(w=MB + 2044), dict(w=2 * MB + 36860), dict(w=4 * MB + 28), dict(w=5 * MB + 8), dict(w=6 * MB - 1020),
+        dict(w=7 * MB + 60), dict(w=7 * MB - 1020), dict(ws=8 * MB, mq=9), dict(ws=7 * MB, mq=9), dict(ws=MB, mq=9)])
+    def test_overlaps(self, lib, change):
+        assert self.call(lib, **change) == -2

@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "fa.h"
 #include "fa_internal.h"
 
@@ -35,6 +37,22 @@ int capacity_of(int max_blocks, int page_size) {
 bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
     const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
     return x < y + nb && y < x + na;
+}
+
+// Whether a result shares memory with an operand or with another result (buffers that are not given share none).
+struct Buffer {
+    const void *p;
+    int64_t bytes;
+};
+bool clash(std::initializer_list<Buffer> results, std::initializer_list<Buffer> operands) {
+    for (const Buffer *r = results.begin(); r != results.end(); ++r) {
+        if (!r->p) continue;
+        for (const Buffer &o : operands)
+            if (o.p && overlap(r->p, r->bytes, o.p, o.bytes)) return true;
+        for (const Buffer *o = results.begin(); o != r; ++o)
+            if (o->p && overlap(r->p, r->bytes, o->p, o->bytes)) return true;
+    }
+    return false;
 }
 
 // Up to 128 query heads share a key head (a token's rows lie in one MMA tile).
@@ -68,6 +86,11 @@ bool few_rows(int G, int max_q_len) {
 int chunk_tile(int G, int D, int max_q_len) {
     return few_rows(G, max_q_len) ? fa::chunk_rows_tile() : fa::chunk_tile_rows(D);
 }
+
+int64_t pool_bytes(int num_pages, int page_size, int Hkv, int D) {
+    return static_cast<int64_t>(num_pages) * page_size * Hkv * D * 2;
+}
+int64_t table_bytes(int num_seqs, int max_blocks) { return static_cast<int64_t>(num_seqs) * max_blocks * 4; }
 
 size_t chunk_bytes(int R, int D, size_t *ml, size_t *o) {
     const size_t slots = 2 * static_cast<size_t>(fa::kChunkMaxCtas) * R;
@@ -240,6 +263,11 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     st = chunk_params(p, q, block_table, max_blocks_per_seq, page_size, num_pages, cu_seqlens, kv_lens, num_seqs, total, Hq,
                       Hkv, D, scale);
     if (st != FA_OK) return st;
+    const int64_t rows_q = static_cast<int64_t>(total) * Hq, pool = pool_bytes(num_pages, page_size, Hkv, D);
+    if (clash({{out, rows_q * D * 2}, {lse, rows_q * 4}, {workspace, fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len)}},
+              {{q, rows_q * D * 2}, {k_cache, pool}, {v_cache, pool}, {block_table, table_bytes(num_seqs, max_blocks_per_seq)},
+               {cu_seqlens, (num_seqs + int64_t(1)) * 4}, {kv_lens, num_seqs * int64_t(4)}}))
+        return FA_ERR_SHAPE;
     p.out = out;
     p.lse = lse;
     const int R = chunk_tile(p.G, D, max_q_len);
@@ -296,6 +324,13 @@ fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t
     st = chunk_params(p, q, block_table, max_blocks_per_seq, page_size, num_pages, cu_seqlens, kv_lens, num_seqs, total, Hq,
                       Hkv, D, scale);
     if (st != FA_OK) return st;
+    const int64_t rows_q = static_cast<int64_t>(total) * Hq;
+    if (clash({{weights, static_cast<int64_t>(num_seqs) * Hkv * width * 4},
+               {few ? nullptr : workspace, fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len)}},
+              {{q, rows_q * D * 2}, {lse, rows_q * 4}, {k_cache, pool_bytes(num_pages, page_size, Hkv, D)},
+               {block_table, table_bytes(num_seqs, max_blocks_per_seq)}, {cu_seqlens, (num_seqs + int64_t(1)) * 4},
+               {kv_lens, num_seqs * int64_t(4)}}))
+        return FA_ERR_SHAPE;
     p.lse_in = lse;
     p.weights = weights;
     p.width = width;
