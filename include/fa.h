@@ -373,8 +373,8 @@ FA_API fa_status fa_paged_key_weights(const void *q, const void *k_cache, const 
  *   kept         int32 (B, Hkv, budget) output: the old slot of each kept key, rising, then -1.
  *   new_lens     int32 [B] output: min(kv_lens[b], budget).
  *   new_weights  float32 (B, Hkv, width) output: the kept keys' weights in their new slots, zeros after.
- * 1 <= budget <= width <= 2^31 - 2^16, 0 <= recent <= budget. The outputs overlap neither weights nor kv_lens
- * (FA_ERR_SHAPE) nor one another. Lengths that do not fit the table are cut to it and FA_ERR_INDEX is left for fa_device_status;
+ * 1 <= budget <= width <= 2^31 - 2^16, 0 <= recent <= budget. The outputs, k_cache and v_cache overlap neither
+ * weights, kv_lens and block_table nor one another (FA_ERR_SHAPE). Lengths that do not fit the table are cut to it and FA_ERR_INDEX is left for fa_device_status;
  * a row whose table entry is outside the pool does not move (FA_ERR_INDEX too).
  */
 FA_API fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_table,

@@ -46,3 +46,20 @@ class TestKeyWeights:
         dict(w=7 * MB + 60), dict(w=7 * MB - 1020), dict(ws=8 * MB, mq=9), dict(ws=7 * MB, mq=9), dict(ws=MB, mq=9)])
     def test_overlaps(self, lib, change):
         assert self.call(lib, **change) == -2
+
+
+class TestEvict:
+    """weights and new weights: 2 * 2 * 64 * 4 = 1024 bytes, kept 128, lengths 8, table 32, pools 36864."""
+
+    def call(self, lib, **kw):
+        a = dict(kc=MB, vc=2 * MB, bt=3 * MB, mb=4, page=16, pages=9, kv=4 * MB, w=5 * MB, width=64, budget=8, recent=2,
+                 kept=6 * MB, nl=7 * MB, nw=8 * MB, b=2, hk=2, d=64, dt=0)
+        a.update(kw)
+        return lib.fa_paged_evict(*a.values(), None)
+
+    @pytest.mark.parametrize("change", [
+        dict(nl=6 * MB), dict(nl=6 * MB + 124), dict(nw=6 * MB - 1020), dict(kept=8 * MB + 1020), dict(nl=8 * MB + 512), dict(nw=7 * MB + 4),
+        dict(vc=MB), dict(vc=MB + 36848), dict(kc=2 * MB + 16), dict(kept=MB + 36860), dict(nw=2 * MB - 1020), dict(nl=2 * MB),
+        dict(kept=3 * MB + 28), dict(nw=3 * MB), dict(w=2 * MB), dict(kv=MB + 128), dict(bt=2 * MB)])
+    def test_overlaps(self, lib, change):
+        assert self.call(lib, **change) == -2

@@ -366,11 +366,12 @@ fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_tabl
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
         !aligned(weights, 4) || !aligned(kept, 4) || !aligned(new_lens, 4) || !aligned(new_weights, 4))
         return FA_ERR_ALIGN;
-    // the inputs are read again while the results are written
-    const int64_t heads = static_cast<int64_t>(B) * Hkv, w_bytes = heads * width * 4;
-    const struct { const void *p; int64_t n; } results[3] = {{kept, heads * budget * 4}, {new_lens, int64_t(B) * 4}, {new_weights, w_bytes}};
-    for (const auto &r : results)
-        if (overlap(weights, w_bytes, r.p, r.n) || overlap(kv_lens, int64_t(B) * 4, r.p, r.n)) return FA_ERR_SHAPE;
+    // the inputs are read again while the results are written, and K and V rows move side by side
+    const int64_t heads = static_cast<int64_t>(B) * Hkv, w_bytes = heads * width * 4, lens = B * int64_t(4);
+    const int64_t pool = pool_bytes(num_pages, page_size, Hkv, D);
+    if (clash({{kept, heads * budget * 4}, {new_lens, lens}, {new_weights, w_bytes}, {k_cache, pool}, {v_cache, pool}},
+              {{weights, w_bytes}, {kv_lens, lens}, {block_table, table_bytes(B, max_blocks_per_seq)}}))
+        return FA_ERR_SHAPE;
     fa::EvictParams p{};
     p.k_cache = k_cache; p.v_cache = v_cache;
     p.block_table = block_table; p.kv_lens = kv_lens;
