@@ -243,7 +243,8 @@ FA_API fa_status fa_pad(const void *x, const int64_t *indices, int64_t nnz, int6
  *   positions    device int64 [n], each in [0, max_pos). One outside reads row 0 instead (that
  *                output is wrong) and leaves FA_ERR_INDEX for fa_device_status.
  *   q_out, k_out the results, token strides of their own; each may be its input itself (same pointer
- *                and stride), and must not overlap it otherwise.
+ *                and stride). Otherwise they overlap neither an input nor one another (FA_ERR_SHAPE); rows
+ *                of one stride may lie between one another (columns of one buffer).
  * rot_dim: a multiple of 16, 16 <= rot_dim <= D. Strides: multiples of 8 elements, at least H * D
  * (FA_ERR_ALIGN). Every pointer but positions 16-byte aligned. eps >= 0. n == 0 is a successful no-op.
  */
@@ -260,7 +261,7 @@ FA_API fa_status fa_qk_norm_rope(const void *q, int64_t q_stride, const void *k,
  *   q, k, the weights, cos_sin, positions, eps, interleaved: as in the forward.
  *   dq_out, dk_out   gradients of q_out and k_out (token strides of their own).
  *   dq, dk           gradients of q and k, element type `dtype` (token strides of their own; dq may be
- *                    dq_out itself and dk dk_out; no other overlap).
+ *                    dq_out or q itself, and dk dk_out or k, same pointer and stride; no other overlap).
  *   dq_weight,
  *   dk_weight        float32 [D] gradients of the weights, summed over tokens and heads in a fixed
  *                    order; either may be NULL.
@@ -291,7 +292,7 @@ FA_API fa_status fa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void
  *   positions    device int64 [n] as above (of rows of no sequence: anything), or NULL: each token's slot is its
  *                position (they differ once keys have been evicted).
  *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
- *                of (page_size, Hkv, D).
+ *                of (page_size, Hkv, D); the pools overlap neither an input nor one another.
  * The rest as fa_qk_norm_rope.
  */
 FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

@@ -63,3 +63,51 @@ class TestEvict:
         dict(kept=3 * MB + 28), dict(nw=3 * MB), dict(w=2 * MB), dict(kv=MB + 128), dict(bt=2 * MB)])
     def test_overlaps(self, lib, change):
         assert self.call(lib, **change) == -2
+
+
+class TestNorm:
+    """4 tokens; q rows of 4 * 64 * 2 = 512 bytes, k rows of 256; views of a fused buffer: rows of 1024 bytes."""
+
+    def call(self, lib, **kw):
+        a = dict(q=MB, qs=256, k=2 * MB, ks=128, wq=9 * MB, wk=10 * MB, w32=0, cs=3 * MB, rows=64, rot=64, pos=4 * MB, qo=5 * MB,
+                 qos=256, ko=6 * MB, kos=128, n=4, hq=4, hk=2, d=64, eps=1e-6, inter=0, dt=1)
+        a.update(kw)
+        return lib.fa_qk_norm_rope(*a.values(), None)
+
+    @pytest.mark.parametrize("change", [
+        dict(qo=2 * MB), dict(ko=MB), dict(qo=MB + 16), dict(qo=MB - 2032), dict(qo=MB, qos=264), dict(qo=6 * MB), dict(ko=5 * MB + 2032),
+        dict(qo=3 * MB), dict(qo=4 * MB), dict(ko=4 * MB + 16), dict(qo=9 * MB), dict(ko=10 * MB + 112), dict(w32=1, ko=10 * MB + 240),
+        # one fused buffer: q in its bytes 0-511 of a row, k in 512-767
+        dict(qs=512, k=MB + 512, ks=512, qo=MB + 16, qos=512), dict(qs=512, k=MB + 512, ks=512, qo=MB, qos=512, ko=MB + 768 - 16, kos=512, n=3, q=MB + 1024),
+        dict(qs=512, k=MB + 512, ks=512, qo=MB + 512, qos=512), dict(qs=512, k=MB + 512, ks=512, ko=MB + 256, kos=512),
+        dict(qs=512, k=MB + 512, ks=512, qo=MB, qos=256), dict(n=1, qo=MB + 496), dict(n=1, ko=MB + 256)])
+    def test_forward(self, lib, change):
+        assert self.call(lib, **change) == -2
+
+    def paged(self, lib, **kw):
+        a = dict(q=MB, qs=256, k=2 * MB, ks=128, v=7 * MB, vs=128, wq=None, wk=None, w32=0, cs=3 * MB, rows=64, rot=64, pos=None,
+                 qo=5 * MB, qos=256, kc=16 * MB, vc=17 * MB, bt=8 * MB, mb=4, page=16, pages=9, cu=9 * MB, kv=10 * MB, num=2, n=4,
+                 hq=4, hk=2, d=64, eps=1e-6, inter=0, dt=1)
+        a.update(kw)
+        return lib.fa_qk_norm_rope_paged(*a.values(), None)
+
+    @pytest.mark.parametrize("change", [
+        dict(vc=16 * MB), dict(vc=16 * MB + 36848), dict(qo=2 * MB), dict(qo=7 * MB), dict(qo=16 * MB - 2032), dict(qo=17 * MB + 36848),
+        dict(kc=MB), dict(kc=2 * MB - 36848), dict(vc=7 * MB + 1008), dict(kc=8 * MB), dict(vc=9 * MB - 36848), dict(qo=10 * MB),
+        dict(qo=3 * MB), dict(kc=3 * MB), dict(pos=16 * MB)])
+    def test_paged(self, lib, change):
+        assert self.paged(lib, **change) == -2
+
+    def bwd(self, lib, **kw):
+        a = dict(q=MB, qs=256, k=2 * MB, ks=128, wq=9 * MB, wk=10 * MB, w32=0, cs=3 * MB, rows=64, rot=64, pos=4 * MB, dqo=5 * MB,
+                 dqos=256, dko=6 * MB, dkos=128, dq=7 * MB, dqs=256, dk=8 * MB, dks=128, dwq=11 * MB, dwk=12 * MB, ws=16 * MB,
+                 wsb=1 << 30, n=4, hq=4, hk=2, d=64, eps=1e-6, inter=0, dt=1)
+        a.update(kw)
+        return lib.fa_qk_norm_rope_bwd(*a.values(), None)
+
+    @pytest.mark.parametrize("change", [
+        dict(dq=6 * MB), dict(dk=5 * MB), dict(dq=5 * MB + 16), dict(dq=5 * MB, dqs=264), dict(dq=2 * MB), dict(dk=MB), dict(dk=7 * MB),
+        dict(dwq=7 * MB), dict(dwk=11 * MB + 252), dict(dwq=9 * MB), dict(ws=11 * MB), dict(ws=7 * MB), dict(dq=3 * MB), dict(dk=4 * MB),
+        dict(q=5 * MB, dq=5 * MB + 32)])
+    def test_backward(self, lib, change):
+        assert self.bwd(lib, **change) == -2

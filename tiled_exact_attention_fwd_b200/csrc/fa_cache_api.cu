@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <initializer_list>
+#include <numeric>
 
 #include "fa.h"
 #include "fa_internal.h"
@@ -51,6 +52,40 @@ bool clash(std::initializer_list<Buffer> results, std::initializer_list<Buffer> 
             if (o.p && overlap(r->p, r->bytes, o.p, o.bytes)) return true;
         for (const Buffer *o = results.begin(); o != r; ++o)
             if (o->p && overlap(r->p, r->bytes, o->p, o->bytes)) return true;
+    }
+    return false;
+}
+
+// n rows of `width` bytes, `stride` bytes apart (n = 1: a buffer).
+struct RowSet {
+    const void *p;
+    int64_t n, stride, width;
+};
+RowSet one(const void *p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+// Whether a row of a and one of b share memory. Rows of one stride may lie between one another (views of a
+// fused projection): they are compared by their places within the stride, which is exact. So are different strides,
+// within their greatest common divisor, which takes some that interleave for rows that meet.
+bool rows_meet(const RowSet &a, const RowSet &b) {
+    if (!a.p || !b.p || !overlap(a.p, (a.n - 1) * a.stride + a.width, b.p, (b.n - 1) * b.stride + b.width)) return false;
+    if (a.n == 1 && b.n == 1) return true;
+    const int64_t g = a.n == 1 ? b.stride : (b.n == 1 ? a.stride : std::gcd(a.stride, b.stride));
+    int64_t d = (static_cast<const char *>(b.p) - static_cast<const char *>(a.p)) % g;
+    if (d < 0) d += g;
+    return d < a.width || d + b.width > g;
+}
+bool same_rows(const RowSet &a, const RowSet &b) { return a.p == b.p && a.stride == b.stride && a.width == b.width; }
+// Whether a result of a norm meets an operand or another result; it may be one of its own operands `in` itself.
+struct NormResult {
+    RowSet rows;
+    RowSet in[2];
+};
+bool norm_clash(std::initializer_list<NormResult> results, std::initializer_list<RowSet> operands) {
+    for (const NormResult *r = results.begin(); r != results.end(); ++r) {
+        for (const RowSet &o : operands)
+            if (rows_meet(r->rows, o) && !(same_rows(r->rows, o) && ((r->in[0].p && same_rows(r->in[0], o)) || (r->in[1].p && same_rows(r->in[1], o)))))
+                return true;
+        for (const NormResult *o = results.begin(); o != r; ++o)
+            if (rows_meet(r->rows, o->rows)) return true;
     }
     return false;
 }
@@ -155,6 +190,11 @@ fa_status fa_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_
     if (!aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
         !aligned(positions, 8))
         return FA_ERR_ALIGN;
+    const int64_t wq = Hq * int64_t(D) * 2, wk = Hkv * int64_t(D) * 2, weight = D * (weight_fp32 ? 4 : 2);
+    const RowSet rq{q, n, q_stride * 2, wq}, rk{k, n, k_stride * 2, wk}, none{};
+    if (norm_clash({{{q_out, n, q_out_stride * 2, wq}, {rq, none}}, {{k_out, n, k_out_stride * 2, wk}, {rk, none}}},
+                   {rq, rk, one(q_weight, weight), one(k_weight, weight), one(cos_sin, max_pos * rot_dim * 4), one(positions, n * 8)}))
+        return FA_ERR_SHAPE;
     fa::QkNormParams p{};
     p.q = q; p.k = k;
     p.q_stride = q_stride; p.k_stride = k_stride;
@@ -185,6 +225,14 @@ fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const void *k, 
         !aligned(k_weight, 16) || !aligned(positions, 8) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) ||
         !aligned(kv_lens, 4))
         return FA_ERR_ALIGN;
+    const int64_t wq = Hq * int64_t(D) * 2, wk = Hkv * int64_t(D) * 2, weight = D * (weight_fp32 ? 4 : 2);
+    const int64_t pool = pool_bytes(num_pages, page_size, Hkv, D);
+    const RowSet rq{q, n, q_stride * 2, wq}, none{};
+    if (norm_clash({{{q_out, n, q_out_stride * 2, wq}, {rq, none}}, {one(k_cache, pool), {none, none}}, {one(v_cache, pool), {none, none}}},
+                   {rq, {k, n, k_stride * 2, wk}, {v, n, v_stride * 2, wk}, one(q_weight, weight), one(k_weight, weight),
+                    one(cos_sin, max_pos * rot_dim * 4), one(positions, n * 8), one(block_table, table_bytes(num_seqs, max_blocks_per_seq)),
+                    one(cu_seqlens, (num_seqs + int64_t(1)) * 4), one(kv_lens, num_seqs * int64_t(4))}))
+        return FA_ERR_SHAPE;
     fa::QkNormParams p{};
     p.q = q; p.k = k; p.v = v;
     p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
@@ -226,6 +274,14 @@ fa_status fa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, in
     if (!aligned(dq_out, 16) || !aligned(dk_out, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(q_weight, 16) ||
         !aligned(k_weight, 16) || !aligned(positions, 8) || !aligned(workspace, 16))
         return FA_ERR_ALIGN;
+    const int64_t wq = Hq * int64_t(D) * 2, wk = Hkv * int64_t(D) * 2, weight = D * (weight_fp32 ? 4 : 2);
+    const RowSet rq{q, n, q_stride * 2, wq}, rk{k, n, k_stride * 2, wk}, gq{dq_out, n, dq_out_stride * 2, wq},
+        gk{dk_out, n, dk_out_stride * 2, wk}, none{};
+    if (norm_clash({{{dq, n, dq_stride * 2, wq}, {gq, rq}}, {{dk, n, dk_stride * 2, wk}, {gk, rk}}, {one(dq_weight, D * 4), {none, none}},
+                    {one(dk_weight, D * 4), {none, none}}, {one(weights ? workspace : nullptr, fa_qk_norm_rope_bwd_workspace(D)), {none, none}}},
+                   {rq, rk, gq, gk, one(q_weight, weight), one(k_weight, weight), one(cos_sin, max_pos * rot_dim * 4),
+                    one(positions, n * 8)}))
+        return FA_ERR_SHAPE;
     fa::QkNormParams p{};
     p.q = q; p.k = k;
     p.q_stride = q_stride; p.k_stride = k_stride;
