@@ -162,3 +162,53 @@ def test_append_with_rows_of_no_sequence(cuda_device, hq, hk, D, behind):
         assert bool((out[total:] == 7.0).all())
         for pool in (kc, vc):
             assert int((pool != 3.0).any(-1).any(-1).sum()) == total  # the tokens' rows, and no others
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,hq,hk,D,rot,dtype,inter", [
+    (1, 2, 1, 32, 32, "bf16", False), (37, 5, 2, 64, 48, "fp16", True), (700, 16, 4, 128, 128, "bf16", False),
+    (2100, 3, 3, 256, 64, "bf16", True)])
+def test_norm_results_in_place_and_between_one_another(cuda_device, tokens, hq, hk, D, rot, dtype, inter):
+    """Results as columns of one buffer, gradients over what they are formed from, through the C entries: the bits of dense
+    results, and nothing between them touched."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, dt, lib = cuda_device, DT[dtype], fa.lib()
+    q, k, v, wq, wk, cs, pos = norm_inputs(tokens, hq, hk, D, rot, dt, dt, True, 13)
+    wq, wk, cs, pos = (t.to(dev) for t in (wq, wk, cs, pos))
+    cols = hq + 2 * hk
+
+    def fused(a, b):  # views like norm_inputs' fused ones, the last columns 9
+        x = torch.full((tokens, cols, D), 9.0, dtype=dt, device=dev)
+        x[:, :hq], x[:, hq:hq + hk] = a, b
+        return x, x[:, :hq], x[:, hq:hq + hk]
+
+    _, fq, fk = fused(q.to(dev), k.to(dev))
+    gq, gk = fa_inputs.normal((tokens, hq, D), dt, 91).to(dev), fa_inputs.normal((tokens, hk, D), dt, 92).to(dev)
+    yq, yk = fa.fa_qk_norm_rope(fq, fk, wq, wk, cs, pos, eps=1e-5, interleaved=inter)
+    buf, oq, ok = fused(torch.zeros_like(gq), torch.zeros_like(gk))
+    fa.fa_qk_norm_rope(fq, fk, wq, wk, cs, pos, eps=1e-5, interleaved=inter, q_out=oq, k_out=ok)
+    assert torch.equal(oq, yq) and torch.equal(ok, yk) and bool((buf[:, hq + hk:] == 9).all())
+    want = fa.fa_qk_norm_rope_bwd(fq, fk, wq, wk, cs, pos, gq, gk, eps=1e-5, interleaved=inter)
+    ws = torch.empty(lib.fa_qk_norm_rope_bwd_workspace(D), dtype=torch.uint8, device=dev)
+
+    def call(xq, xk, dyq, dyk, dq, dk):
+        dw = torch.full((2, D), float("nan"), device=dev)
+        st = lib.fa_qk_norm_rope_bwd(
+            xq.data_ptr(), xq.stride(0), xk.data_ptr(), xk.stride(0), wq.data_ptr(), wk.data_ptr(), 0, cs.data_ptr(), cs.shape[0],
+            rot, pos.data_ptr(), dyq.data_ptr(), dyq.stride(0), dyk.data_ptr(), dyk.stride(0), dq.data_ptr(), dq.stride(0),
+            dk.data_ptr(), dk.stride(0), dw[0].data_ptr(), dw[1].data_ptr(), ws.data_ptr(), ws.numel(), tokens, hq, hk, D, 1e-5,
+            int(inter), int(dtype == "bf16"), torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        for got, ref in zip((dq, dk, dw[0], dw[1]), want):
+            assert torch.equal(got, ref)
+
+    buf, oq, ok = fused(torch.zeros_like(gq), torch.zeros_like(gk))
+    call(fq, fk, gq, gk, oq, ok)  # columns of a buffer
+    assert bool((buf[:, hq + hk:] == 9).all())
+    buf, oq, ok = fused(gq, gk)
+    call(fq, fk, oq, ok, oq, ok)  # over the gradients that come in
+    assert bool((buf[:, hq + hk:] == 9).all())
+    buf, oq, ok = fused(q.to(dev), k.to(dev))
+    call(oq, ok, gq, gk, oq, ok)  # over q and k
+    assert bool((buf[:, hq + hk:] == 9).all())
+    assert fa.fa_device_status()[0] == 0
