@@ -212,3 +212,17 @@ def test_norm_results_in_place_and_between_one_another(cuda_device, tokens, hq, 
     call(oq, ok, gq, gk, oq, ok)  # over q and k
     assert bool((buf[:, hq + hk:] == 9).all())
     assert fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("budget,recent", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (65, 0), (0, 0), (-1, 0), (-2 ** 31, 0), (4, 5), (4, -1)])
+def test_evict_refuses_its_numbers_before_it_allocates(cuda_device, budget, recent):
+    """(8 * 8 heads of 2^31 kept slots would be 550 GB.)"""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev = cuda_device
+    kc, vc = (torch.zeros(32, 16, 8, 32, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    bt = torch.arange(32, dtype=torch.int32, device=dev).view(8, 4)
+    lens = torch.full((8,), 20, dtype=torch.int32, device=dev)
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_paged_evict(kc, vc, bt, lens, torch.zeros(8, 8, 64, device=dev), budget, recent)
+    assert e.value.status == -2

@@ -9,6 +9,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
+
 #include "fa.h"
 
 namespace {
@@ -293,7 +295,9 @@ std::tuple<int, Tensor, Tensor, Tensor> paged_evict(const Tensor &k_cache, const
     weights_arg(weights, g, dev);
     const fa_dtype dtype = dtype_code(k_cache);
     const c10::cuda::OptionalCUDAGuard guard(dev);
-    const Tensor kept = fresh({g.num, g.Hkv, budget > 0 ? budget : 0}, at::kInt, kv_lens);
+    // (a budget that the call below refuses allocates no more than one that it takes)
+    const int64_t held = std::clamp<int64_t>(budget, 0, weights.size(2));
+    const Tensor kept = fresh({g.num, g.Hkv, held}, at::kInt, kv_lens);
     const Tensor new_lens = fresh_like(kv_lens), new_weights = fresh_like(weights);
     const int st = fa_paged_evict(k_cache.data_ptr(), v_cache.data_ptr(), g.table, g.max_blocks, g.page_size, g.num_pages,
                                   g.kv_lens, static_cast<const float *>(weights.data_ptr()), weights.size(2), budget, recent,
