@@ -111,3 +111,19 @@ class TestNorm:
         dict(q=5 * MB, dq=5 * MB + 32)])
     def test_backward(self, lib, change):
         assert self.bwd(lib, **change) == -2
+
+
+@pytest.mark.parametrize("built", [True, False])
+def test_binding_that_does_not_load(lib, monkeypatch, tmp_path, built):
+    """A compiled binding that is there but does not load (built against another torch) is not called missing."""
+    import sys
+
+    import tiled_exact_attention_fwd_b200 as fa
+    monkeypatch.setattr(fa, "_ext", None)
+    monkeypatch.delattr(fa, "_fa_torch", raising=False)
+    monkeypatch.setitem(sys.modules, fa.__name__ + "._fa_torch", None)  # its import raises ImportError
+    if built:
+        (tmp_path / "_fa_torch.so").touch()
+    monkeypatch.setattr(fa, "_HERE", str(tmp_path))
+    with pytest.raises(RuntimeError, match="does not load.*--force" if built else "is not built"):
+        fa._binding()

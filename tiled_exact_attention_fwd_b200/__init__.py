@@ -439,7 +439,10 @@ def _binding():
         try:
             from . import _fa_torch
         except ImportError as e:
-            raise RuntimeError("_fa_torch.so is not built; run `python -m tiled_exact_attention_fwd_b200.build`") from e
+            if not os.path.exists(os.path.join(_HERE, "_fa_torch.so")):
+                raise RuntimeError("_fa_torch.so is not built; run `python -m tiled_exact_attention_fwd_b200.build`") from e
+            raise RuntimeError(f"_fa_torch.so does not load ({e}); it belongs to the torch it was built against: run "
+                               "`python -m tiled_exact_attention_fwd_b200.build --force`") from e
         _ext = _fa_torch
     return _ext
 
