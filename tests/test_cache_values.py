@@ -1,5 +1,6 @@
 """The operators around a paged cache on values that the draws of test_cache_ops.py do not hold, against
-the same definitions in 64 bits and with its tolerances: NaN and infinities in what a row sees."""
+the same definitions in 64 bits and with its tolerances: NaN and infinities in what a row sees, scores that grow
+along the keys, other scales; results in place; calls beside one another."""
 import math
 
 import pytest
@@ -7,7 +8,7 @@ import torch
 
 import fa_inputs
 from oracle import cache as oc
-from test_cache_ops import DT, U, chunk_inputs, half_step, norm_inputs, on, pools, round_tol, score_tol, within
+from test_cache_ops import CHUNK, DT, U, chunk_inputs, half_step, norm_inputs, on, pools, round_tol, same, score_tol, within
 
 
 def check(dev, q, kc, vc, bt, cu, lens, max_q, dt, causal=True, scale=None):
@@ -23,7 +24,10 @@ def check(dev, q, kc, vc, bt, cu, lens, max_q, dt, causal=True, scale=None):
     assert fa.fa_device_status()[0] == 0
     within(out, ref, half_step(dt) * ref.abs() + (half_step(dt) + 2 * e.t()[..., None]) * size + 2.0 ** -25, "out")
     within(lse, rl, e + 2.0 ** -23 * rl.abs(), "lse")
-    within(w, add, (2.0 ** -19 * (most + 1) + 1024 * U) * add, "weights")
+    # A row's weight below fp32's smallest normal number, 2^-126 = 1.18e-38, counts as 0 (2.4e-40 of a sum of 6.0e-38 goes
+    # so): a sum loses at most that much for each of its rows, which no tolerance relative to the sum covers.
+    flushed = max_q * (q.shape[1] // kc.shape[2]) * 2.0 ** -126
+    within(w, add, (2.0 ** -19 * (most + 1) + 1024 * U) * add + flushed, "weights")
     return out, lse, w
 
 
@@ -226,3 +230,84 @@ def test_evict_refuses_its_numbers_before_it_allocates(cuda_device, budget, rece
     with pytest.raises(fa.FAError) as e:
         fa.fa_paged_evict(kc, vc, bt, lens, torch.zeros(8, 8, 64, device=dev), budget, recent)
     assert e.value.status == -2
+
+
+# Rows of a step kernel: single tokens; two row tiles of an item (one at D = 256); one, whose key tiles two warpgroups share.
+GROWING = {"few": (1, 4, 2), "two tiles": (130, 2, 2), "one tile": (20, 8, 2)}
+
+
+def growing_inputs(kind, D, count=64, kv=1000):
+    """Sequences over one another's pages whose key j is larger by 2.2 for every 128 keys before it: the largest score of a
+    window of 128 keys then grows by about the 8 (in log2 units) from which on the running maximum moves."""
+    n, hq, hk = GROWING[kind]
+    q, kc, vc, bt, _, _ = chunk_inputs([n] * count, [kv], hq, hk, D, 16, "bf16", 19 + D, behind=0)
+    for j in range(kv):
+        kc[bt[0, j // 16], j % 16] *= 1 + 2.2 * (j // 128)
+    cu = fa_inputs.cu_seqlens_from_lengths([n] * count)
+    return q, kc, vc, bt.expand(count, -1).contiguous(), cu, torch.tensor([kv - 3 * b for b in range(count)], dtype=torch.int32), n
+
+
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("kind", list(GROWING))
+def test_growing_inputs_grow(kind, D):
+    """In every window but the first, some rows' largest score is more than 8 over all that came before, and some rows' is
+    not: such a row moves its maximum there wherever the split began its run. And a run holds several steps: there are
+    more than 4 times as many (of up to 128 keys) as SMs."""
+    n, hq, hk = GROWING[kind]
+    q, kc, _, bt, _, lens, _ = growing_inputs(kind, D)
+    k = oc.token_rows(kc, bt, 0, 1000)
+    z = torch.einsum("thd,khd->thk", q.double(), k.repeat_interleave(hq // hk, 1)) * math.log2(math.e) / math.sqrt(D)
+    z = torch.nn.functional.pad(z[..., :int(lens[-1]) - n], (0, -(int(lens[-1]) - n) % 128), value=-math.inf)  # keys that all rows see
+    most = z.view(*z.shape[:2], -1, 128).amax(-1)
+    moves = most[..., 1:] > most.cummax(-1).values[..., :-1] + 8
+    share = moves.double().mean((0, 1))[:5]  # of the rows, in each whole window
+    assert bool((share > 0.05).all()) and bool((share < 0.95).all())
+    if kind != "few":  # 32 rows of a warp: some move, some do not
+        warps = moves[..., :5].reshape(-1, 5)[:moves.shape[0] * hq // 32 * 32].view(-1, 32, 5)
+        assert bool((warps.any(1) & ~warps.all(1)).double().mean() > 0.5)
+    assert len(lens) * hk * (int(lens[-1]) // 128) > 4 * 148
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+@pytest.mark.parametrize("kind", list(GROWING))
+def test_growing_scores(cuda_device, kind, D):
+    """O and the sums rescaled while the steps run."""
+    *args, n = growing_inputs(kind, D)
+    check(cuda_device, *args, n, torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.3, 1.0])
+@pytest.mark.parametrize("case", [CHUNK[i] for i in (0, 2, 4, 7, 8, 9, 11, 12, 15, 18)])
+def test_scale(cuda_device, case, scale):
+    new, kv, hq, hk, D, page, dtype, causal = case
+    inputs = chunk_inputs(new, kv, hq, hk, D, page, dtype, 27 + sum(kv), behind=0)
+    check(cuda_device, *inputs, max(new), DT[dtype], causal=causal, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,hq,hk,D", [(3000, 8, 2, 128), (40, 4, 4, 64)])
+def test_gradients_replayed_while_eager_calls_run(cuda_device, tokens, hq, hk, D):
+    """A captured backward replayed on one stream while eager ones run on two others, many of them in flight."""
+    import tiled_exact_attention_fwd_b200 as fa
+    q, k, v, wq, wk, cs, pos = (None if t is None else on(cuda_device, t) for t in
+                                norm_inputs(tokens, hq, hk, D, D, torch.bfloat16, torch.bfloat16, True, 3))
+    grads = [(torch.randn_like(q), torch.randn_like(k)) for _ in range(3)]
+    wants = [fa.fa_qk_norm_rope_bwd(q, k, wq, wk, cs, pos, *g) for g in grads]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.fa_qk_norm_rope_bwd(q, k, wq, wk, cs, pos, *grads[0])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    eager, kept = [], []
+    for _ in range(25):
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+            kept.append([t.clone() for t in got])
+        for i in (1, 2):
+            with torch.cuda.stream(streams[i]):
+                eager.append((i, fa.fa_qk_norm_rope_bwd(q, k, wq, wk, cs, pos, *grads[i])))
+    torch.cuda.synchronize()
+    assert all(same(t, wants[0]) for t in kept) and all(same(t, wants[i]) for i, t in eager)
