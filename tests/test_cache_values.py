@@ -8,7 +8,7 @@ import torch
 
 import fa_inputs
 from oracle import cache as oc
-from test_cache_ops import CHUNK, DT, U, chunk_inputs, half_step, norm_inputs, on, pools, round_tol, same, score_tol, within
+from test_cache_ops import CHUNK, DT, U, angles, chunk_inputs, half_step, norm_inputs, on, pools, round_tol, same, score_tol, within
 
 
 def check(dev, q, kc, vc, bt, cu, lens, max_q, dt, causal=True, scale=None):
@@ -311,3 +311,109 @@ def test_gradients_replayed_while_eager_calls_run(cuda_device, tokens, hq, hk, D
                 eager.append((i, fa.fa_qk_norm_rope_bwd(q, k, wq, wk, cs, pos, *grads[i])))
     torch.cuda.synchronize()
     assert all(same(t, wants[0]) for t in kept) and all(same(t, wants[i]) for i, t in eager)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("few", [True, False])
+def test_replayed_over_other_lengths(cuda_device, few):
+    """A captured step (append, attention, weights, eviction) replayed after the lengths, the offsets and the table have been
+    changed in place, with sequences that left the batch: the bits of eager calls, rows of no sequence as they were."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, B, cols, page, hq, hk, D = cuda_device, 6, 40, 16, 8, 2, 64
+    total = 6 if few else 200
+    g = fa_inputs.generator(3)
+    x = [fa_inputs.normal((total, h, D), torch.bfloat16, 40 + h).to(dev) for h in (hq, hk, hk)]
+    pools0 = [torch.randn(B * cols, page, hk, D, generator=g).bfloat16().to(dev) for _ in range(2)]
+    kc, vc = (t.clone() for t in pools0)
+    bt = torch.arange(B * cols, dtype=torch.int32, device=dev).view(B, cols).contiguous()
+    cu, lens = torch.zeros(B + 1, dtype=torch.int32, device=dev), torch.zeros(B, dtype=torch.int32, device=dev)
+    cs, q, out = angles(cols * page, D).to(dev), torch.empty_like(x[0]), torch.empty_like(x[0])
+    lse, w = torch.empty(hq, total, device=dev), torch.empty(B, hk, cols * page, device=dev)
+
+    def reset():
+        kc.copy_(pools0[0]), vc.copy_(pools0[1]), w.zero_()
+        for t in (q, out, lse):
+            t.fill_(7.0)
+
+    def step():
+        fa.fa_qk_norm_rope_paged(*x, None, None, cs, None, kc, vc, bt, cu, lens, q_out=q)
+        fa.fa_fwd_paged_chunk(q, kc, vc, bt, cu, lens, 1 if few else 150, out=out, lse=lse)
+        fa.fa_paged_key_weights(q, kc, bt, cu, lens, 1 if few else 150, lse, w)
+        return fa.fa_paged_evict(kc, vc, bt, lens, w, 300, 40)
+
+    new = [[1, 1, 1, 1, 1, 1], [1, 0, 1, 1, 0, 0], [0] * 6] if few else [[50, 1, 0, 149, 0, 0], [150, 0, 1, 1, 20, 3], [0, 0, 0, 0, 0, 7]]
+    kv = [[100, 640, 1, 320, 17, 400], [640, 5, 555, 2, 0, 301], [640] * 6] if few else [[600, 1, 30, 640, 0, 9], [150, 640, 400, 2, 90, 33], [640] * 6]
+
+    def lay(i):
+        cu.copy_(fa_inputs.cu_seqlens_from_lengths(new[i])), lens.copy_(torch.tensor(kv[i], dtype=torch.int32))
+        bt.copy_(torch.randperm(B * cols, generator=fa_inputs.generator(i)).view(B, cols).int())
+        reset()
+
+    lay(0)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        results = step()
+    for i in (1, 2, 0):
+        lay(i)
+        want = [t.clone() for t in (*step(), q, out, lse, w, kc, vc)]
+        reset()
+        graph.replay()
+        assert same(want, [*results, q, out, lse, w, kc, vc])
+        live = sum(new[i])
+        assert all(bool((t[live:] == 7.0).all()) for t in (q, out, lse.t()))
+    assert fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wtype", [torch.float32, torch.bfloat16])
+def test_weights_of_one_of_the_two(cuda_device, wtype):
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, dt = cuda_device, torch.bfloat16
+    q, k, v, wq, wk, cs, pos = norm_inputs(50, 4, 2, 64, 64, dt, wtype, False, 3)
+    gq, gk = fa_inputs.normal(q.shape, dt, 1), fa_inputs.normal(k.shape, dt, 2)
+    for a, b in ((wq, None), (None, wk)):
+        args = [on(dev, t) for t in (q, k, a, b, cs, pos)]
+        for got, x, w in zip(fa.fa_qk_norm_rope(*args), (q, k), (a, b)):
+            ref, size = oc.norm_rope(x, w, cs, pos, 1e-6, False)
+            within(got, ref, round_tol(ref, size, dt, 32), "norm_rope")
+        got = fa.fa_qk_norm_rope_bwd(*args, gq.to(dev), gk.to(dev), stream=0)  # (stream 0: the default one)
+        for x, w, dy, dx, dw in ((q, a, gq, got[0], got[2]), (k, b, gk, got[1], got[3])):
+            rx, rw, sx, sw = oc.norm_rope_bwd(x, w, cs, pos, dy, 1e-6, False)
+            within(dx, rx, round_tol(rx, sx, dt, 64), "dx")
+            assert (dw is None) == (w is None)
+            if w is not None:
+                within(dw, rw, 97 * U * sw, "dw")
+    assert fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [1, 20])
+def test_longest_cache(cuda_device, new):
+    """2^31 - 2^20 keys, all pages one page of 2^20: the attention of that page, 2047 times its sum; each key's
+    weight a 2047th. (The new tokens see all keys, so every position up to the last counts.)"""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, page, pages, D = cuda_device, 1 << 20, 2047, 32
+    kc, vc = (fa_inputs.normal((1, page, 1, D), torch.bfloat16, s).to(dev) for s in (1, 2))
+    vc += 1
+    q = fa_inputs.normal((new, 2, D), torch.bfloat16, 3).to(dev)
+    bt = torch.zeros(1, pages, dtype=torch.int32, device=dev)
+    cu, lens = torch.tensor([0, new], dtype=torch.int32, device=dev), torch.tensor([page * pages], dtype=torch.int32, device=dev)
+    out, lse = fa.fa_fwd_paged_chunk(q, kc, vc, bt, cu, lens, new, causal=False)
+    z = torch.einsum("thd,kd->thk", q.double(), kc[0, :, 0].double()) / math.sqrt(D)
+    rl, p = torch.logsumexp(z, -1), torch.softmax(z, -1)
+    v = vc[0, :, 0].double()
+    ref, size = p @ v, p @ v.abs()
+    # A CTA's run is 2^31 / 148 keys, 113 thousand steps of 128; each adds up to 8 times (16 keys an MMA) to a sum of 32 bits,
+    # and an MMA may cut what does not fit instead of rounding it: 2^-23 each at most
+    long = 2 ** 31 / 128 / 148 * 8 * 2 * U
+    e = 2.0 ** -20 * (z.abs().amax() + 1) * 8
+    within(out, ref.cpu(), (half_step(torch.bfloat16) * (ref.abs() + size) + (2 * e + 2 * long) * size).cpu(), "out")
+    within(lse, (rl + math.log(pages)).t().cpu(), (e + long + 2.0 ** -20).cpu().expand(2, new), "lse")
+    w = torch.zeros(1, 1, page * pages, device=dev)
+    fa.fa_paged_key_weights(q, kc, bt, cu, lens, new, lse, w, causal=False)
+    each = (p.sum((0, 1)) / pages)  # of a page's keys
+    for i in (0, 1, 1023, 2045, 2046):
+        got = w[0, 0, i * page:(i + 1) * page].double()
+        assert bool(((got - each).abs() <= each * (2 * e + 2 * long)).all())
+    assert bool((w != 0).all()) and fa.fa_device_status()[0] == 0
