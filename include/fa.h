@@ -345,7 +345,8 @@ FA_API fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const vo
  *   key j of exp(scale * q.k_j - lse).
  *   q, k_cache, block_table, cu_seqlens, kv_lens, max_q_len, scale, causal: as fa_fwd_paged_chunk.
  *   lse          (Hq, total) float32 that fa_fwd_paged_chunk returned for the same arguments (-inf
- *                rows give nothing).
+ *                rows give nothing). Where a row's lse is NaN the keys that it sees get NaN, and so does a
+ *                key with which a row that sees it has a score of NaN, whatever its lse.
  *   weights      float32 (num_seqs, Hkv, width), width >= max_blocks_per_seq * page_size; slots at and
  *                past kv_lens[b] are not touched. Each sum is formed in a fixed order. Neither they nor
  *                the workspace overlap another argument (FA_ERR_SHAPE).

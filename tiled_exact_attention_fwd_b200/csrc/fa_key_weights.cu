@@ -273,9 +273,9 @@ key_weights_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const ChunkPar
                             ls[i][k] = 0.f;
                             if (r < w.s.n * p.G) {
                                 const float x = p.lse_in[static_cast<int64_t>(w.h * p.G + r % p.G) * p.total + w.s.q0 + r / p.G];
-                                ls[i][k] = x * 1.4426950408889634f;
-                                // a row that saw nothing gives no weight
-                                lim[i][k] = x == -INFINITY ? 0 : token_keys<CAUSAL>(w.s, r / p.G);
+                                // a row that saw nothing above -inf gives no weight: 2^(s - inf)
+                                ls[i][k] = x == -INFINITY ? INFINITY : x * 1.4426950408889634f;
+                                lim[i][k] = token_keys<CAUSAL>(w.s, r / p.G);
                             }
                         }
                     }

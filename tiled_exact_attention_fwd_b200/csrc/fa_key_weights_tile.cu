@@ -40,9 +40,10 @@ struct KtCfg {
     static constexpr int OFF_Q = KB * K_BYTES;
     static constexpr int OFF_L = OFF_Q + NQ * TILE;  // NQ x 128 floats
     static constexpr int OFF_SUM = OFF_L + NQ * BN * 4;  // 2 x KEYS floats: the second column half's sums
-    static constexpr int OFF_ODD = OFF_SUM + 2 * KEYS * 4;  // NQ flags: rows of the tile whose lse is NaN or -inf
-    static constexpr int OFF_BAR = OFF_ODD + 16;
-    static_assert(NQ <= 4, "flags");
+    // Items by turns: how many keys the item's rows of NaN lse see. The -lse are at most NQ steps, so as many items, ahead.
+    static constexpr int LIMITS = 8, OFF_NAN = OFF_SUM + 2 * KEYS * 4;
+    static constexpr int OFF_BAR = OFF_NAN + LIMITS * 4;
+    static_assert(NQ < LIMITS, "limits of items that are still worked on");
     static constexpr int BARS = 2 * KB + 3 * NQ + 4 * KT + 1;
     static constexpr int OFF_START = OFF_BAR + BARS * 8;
     static constexpr int OFF_TMEM = OFF_START + static_cast<int>(sizeof(ChunkStart));
@@ -243,7 +244,7 @@ key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *sL = reinterpret_cast<float *>(smem + C::OFF_L);
-    int *sOdd = reinterpret_cast<int *>(smem + C::OFF_ODD);
+    int *sNan = reinterpret_cast<int *>(smem + C::OFF_NAN);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR), *k_empty = k_full + KB;
     uint64_t *q_full = k_empty + KB, *q_empty = q_full + NQ, *l_full = q_empty + NQ;
     uint64_t *s_full = l_full + NQ, *s_free = s_full + 2 * KT, *drain = s_free + 2 * KT;  // [tile][buffer]
@@ -348,31 +349,32 @@ key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     } else if (warp == W_L) {
         // ------------------------------------------------------------ -lse of the rows, log2 units
         bool ok = true;
-        int u = 0;
-        for (bool more = w.begin(p, *start); more && ok; more = w.next(p)) {
+        int u = 0, it = 0;
+        for (bool more = w.begin(p, *start); more && ok; more = w.next(p), ++it) {
+            int nan = 0;  // a row whose lse is NaN: keys [0, nan) are seen by one
             for (int t = w.t0; t < w.t1; ++t, ++u) {
                 const int st = u % NQ;
                 float x[4];
-                bool odd = false;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int c = lane + 32 * k, ti = c / p.G, i = t * T + ti;
                     x[k] = -INFINITY;  // no row: no weight
                     if (ti < T && i < w.s.n) {
                         const float v = __ldg(p.lse_in + static_cast<int64_t>(w.h * p.G + c - ti * p.G) * p.total + w.s.q0 + i);
-                        // a row that saw nothing gives no weight either
-                        if (v != -INFINITY) x[k] = v * -1.4426950408889634f;
-                        odd |= !(v > -INFINITY);
+                        // A row that saw nothing gives no weight either. Nor does one whose lse is NaN in the sums: with NaN in
+                        // them its masked keys would be NaN too (-inf + NaN); those that it sees become so at the end.
+                        if (v > -INFINITY) x[k] = v * -1.4426950408889634f;
+                        if (v != v) nan = max(nan, token_keys<CAUSAL>(w.s, i));
                     }
                 }
-                odd = __any_sync(0xffffffffu, odd);
                 if (u >= NQ && !__all_sync(0xffffffffu, wait_bounded(&q_empty[st], ((u / NQ) - 1) & 1, abort_flag, lim, 793))) {
                     ok = false;
                     break;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) sL[st * BN + lane + 32 * k] = x[k];
-                if (lane == 0) sOdd[st] = odd;
+                nan = __reduce_max_sync(0xffffffffu, nan);
+                if (lane == 0) sNan[it % C::LIMITS] = nan;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&l_full[st]);
             }
@@ -459,41 +461,26 @@ key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     // columns [lo, hi) are rows that see the key
                     const int lo = (sees - t * T) * p.G - half * COLS, hi = min(T, w.s.n - t * T) * p.G - half * COLS;
                     const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < COLS;
-                    const float4 *nl = reinterpret_cast<const float4 *>(sL + st * BN + half * COLS);
-                    if (sOdd[st]) {
-                        // NaN and -inf among the rows' -lse: added to a masked score of -inf, or to a score of NaN, they
-                        // would give NaN where there is no weight. One column at a time (rare, and small code).
-                        const float *l = reinterpret_cast<const float *>(nl);
-#pragma unroll 1
-                        for (int c = 0; c < COLS; ++c) {
-                            uint32_t sr[1];
-                            tmem_ld1(at_tmem + buf * BN + c, sr);
-                            tmem_ld_wait();
-                            tmem_reg_fence<1>(sr);
-                            const float x = ex2_approx(fmaf(__uint_as_float(sr[0]), p.scale_log2, l[c]));
-                            if (c >= lo && c < hi && l[c] != -INFINITY) acc[0] = fadd2(acc[0], f2(x, 0.f));
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 32) {  // 32 columns in registers at a time
+                        uint32_t sr[32];
+                        tmem_ld32(at_tmem + buf * BN + c, sr);
+                        tmem_ld_wait();
+                        tmem_reg_fence<32>(sr);
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < lo || c + i >= hi) sr[i] = __float_as_uint(-INFINITY);
                         }
-                    } else {
+                        const float4 *nl = reinterpret_cast<const float4 *>(sL + st * BN + half * COLS + c);
 #pragma unroll
-                        for (int c = 0; c < COLS; c += 32) {  // 32 columns in registers at a time
-                            uint32_t sr[32];
-                            tmem_ld32(at_tmem + buf * BN + c, sr);
-                            tmem_ld_wait();
-                            tmem_reg_fence<32>(sr);
-                            if (masked) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (c + i < lo || c + i >= hi) sr[i] = __float_as_uint(-INFINITY);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 l = nl[c / 4 + i];
-                                float x0, x1, x2, x3;
-                                f2_split(ffma2(f2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1])), c2, f2(l.x, l.y)), x0, x1);
-                                f2_split(ffma2(f2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3])), c2, f2(l.z, l.w)), x2, x3);
-                                acc[(2 * i) & 3] = fadd2(acc[(2 * i) & 3], f2(ex2_approx(x0), ex2_approx(x1)));
-                                acc[(2 * i + 1) & 3] = fadd2(acc[(2 * i + 1) & 3], f2(ex2_approx(x2), ex2_approx(x3)));
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 l = nl[i];
+                            float x0, x1, x2, x3;
+                            f2_split(ffma2(f2(__uint_as_float(sr[4 * i]), __uint_as_float(sr[4 * i + 1])), c2, f2(l.x, l.y)), x0, x1);
+                            f2_split(ffma2(f2(__uint_as_float(sr[4 * i + 2]), __uint_as_float(sr[4 * i + 3])), c2, f2(l.z, l.w)), x2, x3);
+                            acc[(2 * i) & 3] = fadd2(acc[(2 * i) & 3], f2(ex2_approx(x0), ex2_approx(x1)));
+                            acc[(2 * i + 1) & 3] = fadd2(acc[(2 * i + 1) & 3], f2(ex2_approx(x2), ex2_approx(x3)));
                         }
                     }
                     tc_fence_before_sync();
@@ -509,7 +496,7 @@ key_weights_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (half == 1) *other = lo + hi;
             asm volatile("bar.sync %0, 256;" ::"r"(1 + a) : "memory");
             if (half == 1 || !ok || !busy) continue;
-            const float sum = (lo + hi) + *other;
+            const float sum = key < sNan[it % C::LIMITS] ? NAN : (lo + hi) + *other;
             if (!whole)
                 p.part_o[static_cast<int64_t>(w.slot()) * C::KEYS + in] = sum;
             else if (key < w.s.kv)
