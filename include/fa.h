@@ -238,7 +238,8 @@ FA_API fa_status fa_pad(const void *x, const int64_t *indices, int64_t nnz, int6
  *                token are contiguous, tokens lie q_stride / k_stride elements apart (views of a
  *                fused projection work as they are).
  *   q_weight,
- *   k_weight     D weights each, of `dtype` or (weight_fp32 nonzero) float32; NULL: ones.
+ *   k_weight     D weights each, of `dtype` or (weight_fp32 nonzero) float32; NULL: ones (the norm is taken
+ *                all the same).
  *   cos_sin      float32 (max_pos, rot_dim): rot_dim/2 cosines, then rot_dim/2 sines of each position.
  *   positions    device int64 [n], each in [0, max_pos). One outside reads row 0 instead (that
  *                output is wrong) and leaves FA_ERR_INDEX for fa_device_status.

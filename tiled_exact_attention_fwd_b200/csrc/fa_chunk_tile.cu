@@ -20,9 +20,11 @@
 // softmax warp without a row skips the exponentials. An item that the split cuts leaves O, m and l in the workspace.
 //
 // Bound, as the dense forward, by softmax and MMAs waiting for one another (both pipes 54 % busy); measured with
-// the joining: 2048 tokens over 8192 keys (32 heads on 8, D = 128) 220 us, 1.09 PFLOP/s (fa_fwd on a problem of
-// the same products 1.16); 9 sequences of up to 333 tokens over 2777 (D = 64) 51 us, where starting and joining
-// are a third.
+// the joining: 2048 tokens over 8192 keys (32 heads on 8, D = 128) 220 to 240 us in short runs, 1.0 to 1.09 PFLOP/s (fa_fwd on a
+// problem of the same products 1.16), 254 us, 0.95 PFLOP/s, over seconds, when the power cap lowers the clock; first scores
+// after 6, joining 14. 9 sequences of up to 333 tokens over 2777 (D = 64) 51 us: first scores after 5, CTAs that end up to 5
+// apart, joining 9. P in 16 bits makes the error of out against 64 bits 1.4 times that of the output's rounding alone (bf16 2.3e-3
+// beside 1.7e-3).
 #include "fa_chunk.cuh"
 #include "fa_fwd_kernel.cuh"
 

@@ -17,7 +17,9 @@
 // that stay in place are skipped).
 //
 // Measured: 16 sequences of up to 8192 keys, 8 heads of 128, cut to 2048: 71 us, of which the selection 15 and the
-// moving 50 (273 MB: 5.5 TB/s); 3 of 777 to 300: 14 us, both kernels' latency. (Four passes of 8 bits in the
+// moving 50 (273 MB: 5.5 TB/s); 3 of 777 to 300: 14 us, both kernels' latency. One sequence of 32768 keys to 4096 47 us,
+// of 131072 to 16384 194: the selection is then one CTA for each of 8 heads, and past 16384 keys it reads the weights again
+// in each pass. (Four passes of 8 bits in the
 // selection, no overlap of the two kernels: 74 us.)
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -280,9 +282,10 @@ cudaError_t launch_evict(const EvictParams &p, cudaStream_t st) {
     evict_select_kernel<<<dim3(p.Hkv, p.batch), kSelThreads, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // Wider slices are kinder to the memory, narrower ones make more CTAs. 8192 keys cut to 2048, D = 128, slices of
-    // 32 / 64 / 128 / 256 bytes (us): 64 sequences of 8 heads 345 / 263 / 258 / 247, 16 of 8 90 / 74.7 / 72.8 /
-    // 85.9, 2 of 8 25.5 / 28.9 / 40.7 / 60.2.
+    // Wider slices are kinder to the memory, narrower ones make more CTAs. 8192 keys cut to 2048, 8 heads of 128, slices of
+    // 32 / 64 / 128 / 256 bytes (us), the rule's the best of them or within 6 %:
+    //   sequences  2: 25 / 27 / 34 / 51     4: 31 / 33 / 40 / 58      8: 49 / 43 / 53 / 68      12: 68 / 64 / 64 / 91
+    //             16: 86 / 74 / 71 / 92    24: 131 / 114 / 119 / 115  32: 167 / 142 / 136 / 129  64: 330 / 270 / 264 / 251
     const int64_t bytes = static_cast<int64_t>(p.batch) * p.Hkv * p.D * 4;  // of all heads' K and V rows
     if (bytes >= 1024 * 256 && p.D >= 128) return launch_move<256>(p, st);
     if (bytes >= 512 * 128 && p.D >= 64) return launch_move<128>(p, st);

@@ -8,7 +8,7 @@
 // order, and added to the buffer by a plain load and store. Items go to the CTAs in equal runs of
 // row tiles. S is computed transposed, S^T = K Q^T: a thread then holds scores of its own keys, and
 // the sum over rows is an addition in its registers. Bound by reading K once: 64 single tokens over up to 8192
-// keys (32 heads on 8, D = 128) 110 us for 693 MB, 6.3 TB/s; what is left is the start (finding the run; its costs
+// keys (32 heads on 8, D = 128) 110 to 117 us for 693 MB, 5.9 to 6.3 TB/s; what is left is the start (finding the run; its costs
 // are summed in closed form over the key tiles that all rows see: 3 us less than one by one).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

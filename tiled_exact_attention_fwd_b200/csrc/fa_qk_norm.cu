@@ -277,11 +277,12 @@ struct Walk {
 };
 
 // Measured at 8192 tokens of 64 heads of 128 (forward / backward, us): two rows a lane, two CTAs an SM and
-// three slots 51 / 72 (as fast as a plain copy of the forward's bytes, 51); four slots 53 / 71; two slots 53 / 91; four rows in the
+// three slots 51 / 72 to 76, as the inputs lie in memory (as fast as a plain copy of the forward's bytes, 51); four slots 53 / 71; two slots 53 / 91; four rows in the
 // backward 71.6. Three CTAs, whose registers spill, 54.5 / 105; the next rows in registers instead of a ring 60.5 / 86.
-// Runs of neighbouring batches for each warp, against whole tokens by turns: 32 heads beside 8 of 128 38 / 56 against 41 /
-// 60, beside 2 of 64 21 / 34 against 82 / 91 (there the CTAs were shared out by heads, and a token of few heads costs a
-// warp as much as one of many); 32 beside 32, where the tokens divide by the warps, 51 / 72 against 49 / 76.
+// Runs of neighbouring batches for each warp, against whole tokens by turns (timed in turn): 32 heads beside 8 of 128 39 / 55
+// against 42 / 59, beside 2 of 64 23 / 35 against 86 / 92 (there the CTAs were shared out by heads, and a token of few heads
+// costs a warp as much as one of many); 32 beside 32, where the tokens divide by the warps, 51 / 72 against 50 / 76. Appending
+// 4 x 2048 tokens of 32 + 2 x 8 heads of 128: 49 us for 201 MB, 4.1 TB/s; 64 single tokens 6, the host time of the call.
 constexpr int kRows = 2;   // rows a lane takes at a time
 constexpr int kPerSm = 2;  // CTAs an SM
 constexpr int kSlots = 3;  // batches in the ring, one of them being worked on
