@@ -293,7 +293,8 @@ FA_API fa_status fa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void
  *   positions    device int64 [n] as above (of rows of no sequence: anything), or NULL: each token's slot is its
  *                position (they differ once keys have been evicted).
  *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
- *                of (page_size, Hkv, D); the pools overlap neither an input nor one another.
+ *                of (page_size, Hkv, D). K and V pools that overlap lie whole pages apart (FA_ERR_SHAPE), and
+ *                the pages that a call writes overlap nothing else of its arguments.
  * The rest as fa_qk_norm_rope.
  */
 FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -324,7 +325,8 @@ FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const vo
  *   max_q_len    the most new tokens of a sequence. It chooses the kernel and the workspace's size, not the
  *                result.
  *   out          (total, Hq, D); lse (Hq, total) float32 or NULL. Rows of no sequence are left as they
- *                are. Neither they nor the workspace overlap an input or one another (FA_ERR_SHAPE).
+ *                are. Neither they nor the workspace overlap an input or one another (FA_ERR_SHAPE; of the pools,
+ *                the pages that the table names count, which is not checked).
  *   workspace    fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len) bytes, 256-byte aligned, contents
  *                of no matter. Calls that overlap on the GPU (other streams, graphs replayed at the same
  *                time) need one each.
@@ -350,7 +352,7 @@ FA_API fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const vo
  *                key with which a row that sees it has a score of NaN, whatever its lse.
  *   weights      float32 (num_seqs, Hkv, width), width >= max_blocks_per_seq * page_size; slots at and
  *                past kv_lens[b] are not touched. Each sum is formed in a fixed order. Neither they nor
- *                the workspace overlap another argument (FA_ERR_SHAPE).
+ *                the workspace overlap another argument (FA_ERR_SHAPE; pools as above).
  *   workspace    fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len) bytes, 256-byte aligned, contents of
  *                no matter (0 bytes where a key head has at most 16 rows: NULL will do).
  * Calls that overlap on the GPU must share neither `weights` nor the workspace.
@@ -376,8 +378,8 @@ FA_API fa_status fa_paged_key_weights(const void *q, const void *k_cache, const 
  *   kept         int32 (B, Hkv, budget) output: the old slot of each kept key, rising, then -1.
  *   new_lens     int32 [B] output: min(kv_lens[b], budget).
  *   new_weights  float32 (B, Hkv, width) output: the kept keys' weights in their new slots, zeros after.
- * 1 <= budget <= width <= 2^31 - 2^16, 0 <= recent <= budget. The outputs, k_cache and v_cache overlap neither
- * weights, kv_lens and block_table nor one another (FA_ERR_SHAPE). Lengths that do not fit the table are cut to it and FA_ERR_INDEX is left for fa_device_status;
+ * 1 <= budget <= width <= 2^31 - 2^16, 0 <= recent <= budget. The outputs overlap neither weights, kv_lens and
+ * block_table nor one another, and K and V pools that overlap lie whole pages apart (FA_ERR_SHAPE). Lengths that do not fit the table are cut to it and FA_ERR_INDEX is left for fa_device_status;
  * a row whose table entry is outside the pool does not move (FA_ERR_INDEX too).
  */
 FA_API fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_table,

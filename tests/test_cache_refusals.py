@@ -14,8 +14,7 @@ def lib():
 
 
 class TestChunk:
-    """q and out: 4 * 4 * 64 * 2 = 2048 bytes, lse 64, pools 9 * 16 * 2 * 64 * 2 = 36864, table 32, cu_seqlens 12,
-    kv_lens 8."""
+    """q and out: 4 * 4 * 64 * 2 = 2048 bytes, lse 64, table 32, cu_seqlens 12, kv_lens 8."""
 
     def call(self, lib, **kw):
         a = dict(q=MB, kc=2 * MB, vc=3 * MB, bt=4 * MB, mb=4, page=16, pages=9, cu=5 * MB, kv=6 * MB, num=2, total=4, mq=2,
@@ -24,10 +23,10 @@ class TestChunk:
         return lib.fa_fwd_paged_chunk(*a.values(), None)
 
     @pytest.mark.parametrize("change", [
-        dict(out=MB), dict(out=MB + 2032), dict(out=MB - 2032), dict(out=2 * MB + 36848), dict(out=3 * MB), dict(out=4 * MB - 2032),
-        dict(out=4 * MB + 16), dict(out=5 * MB), dict(out=6 * MB), dict(lse=MB), dict(lse=2 * MB - 60), dict(lse=4 * MB + 28),
+        dict(out=MB), dict(out=MB + 2032), dict(out=MB - 2032), dict(out=4 * MB - 2032),
+        dict(out=4 * MB + 16), dict(out=5 * MB), dict(out=6 * MB), dict(lse=MB), dict(lse=4 * MB + 28),
         dict(lse=5 * MB + 8), dict(lse=6 * MB - 60), dict(lse=7 * MB + 2044), dict(lse=7 * MB - 60), dict(out=16 * MB), dict(lse=16 * MB + 4),
-        dict(ws=7 * MB), dict(ws=2 * MB), dict(ws=MB), dict(ws=MB // 2, mq=9, q=MB)])
+        dict(ws=7 * MB), dict(ws=MB), dict(ws=MB // 2, mq=9, q=MB)])
     def test_overlaps(self, lib, change):
         assert self.call(lib, **change) == -2
 
@@ -42,14 +41,14 @@ class TestKeyWeights:
         return lib.fa_paged_key_weights(*a.values(), None)
 
     @pytest.mark.parametrize("change", [
-        dict(w=MB), dict(w=MB - 1020), dict(w=MB + 2044), dict(w=2 * MB + 36860), dict(w=4 * MB + 28), dict(w=5 * MB + 8), dict(w=6 * MB - 1020),
+        dict(w=MB), dict(w=MB - 1020), dict(w=MB + 2044), dict(w=4 * MB + 28), dict(w=5 * MB + 8), dict(w=6 * MB - 1020),
         dict(w=7 * MB + 60), dict(w=7 * MB - 1020), dict(ws=8 * MB, mq=9), dict(ws=7 * MB, mq=9), dict(ws=MB, mq=9)])
     def test_overlaps(self, lib, change):
         assert self.call(lib, **change) == -2
 
 
 class TestEvict:
-    """weights and new weights: 2 * 2 * 64 * 4 = 1024 bytes, kept 128, lengths 8, table 32, pools 36864."""
+    """weights and new weights: 2 * 2 * 64 * 4 = 1024 bytes, kept 128, lengths 8, table 32, pools 9 * 4096."""
 
     def call(self, lib, **kw):
         a = dict(kc=MB, vc=2 * MB, bt=3 * MB, mb=4, page=16, pages=9, kv=4 * MB, w=5 * MB, width=64, budget=8, recent=2,
@@ -59,8 +58,8 @@ class TestEvict:
 
     @pytest.mark.parametrize("change", [
         dict(nl=6 * MB), dict(nl=6 * MB + 124), dict(nw=6 * MB - 1020), dict(kept=8 * MB + 1020), dict(nl=8 * MB + 512), dict(nw=7 * MB + 4),
-        dict(vc=MB), dict(vc=MB + 36848), dict(kc=2 * MB + 16), dict(kept=MB + 36860), dict(nw=2 * MB - 1020), dict(nl=2 * MB),
-        dict(kept=3 * MB + 28), dict(nw=3 * MB), dict(w=2 * MB), dict(kv=MB + 128), dict(bt=2 * MB)])
+        dict(vc=MB), dict(vc=MB + 36848), dict(kc=2 * MB + 16), dict(vc=MB + 4096 + 16), dict(vc=MB - 2048),
+        dict(kept=3 * MB + 28), dict(nw=3 * MB)])
     def test_overlaps(self, lib, change):
         assert self.call(lib, **change) == -2
 
@@ -76,7 +75,7 @@ class TestNorm:
 
     @pytest.mark.parametrize("change", [
         dict(qo=2 * MB), dict(ko=MB), dict(qo=MB + 16), dict(qo=MB - 2032), dict(qo=MB, qos=264), dict(qo=6 * MB), dict(ko=5 * MB + 2032),
-        dict(qo=3 * MB), dict(qo=4 * MB), dict(ko=4 * MB + 16), dict(qo=9 * MB), dict(ko=10 * MB + 112), dict(w32=1, ko=10 * MB + 240),
+        dict(qo=4 * MB), dict(ko=4 * MB + 16), dict(qo=9 * MB), dict(ko=10 * MB + 112), dict(w32=1, ko=10 * MB + 240),
         # one fused buffer: q in its bytes 0-511 of a row, k in 512-767
         dict(qs=512, k=MB + 512, ks=512, qo=MB + 16, qos=512), dict(qs=512, k=MB + 512, ks=512, qo=MB, qos=512, ko=MB + 768 - 16, kos=512, n=3, q=MB + 1024),
         dict(qs=512, k=MB + 512, ks=512, qo=MB + 512, qos=512), dict(qs=512, k=MB + 512, ks=512, ko=MB + 256, kos=512),
@@ -92,9 +91,8 @@ class TestNorm:
         return lib.fa_qk_norm_rope_paged(*a.values(), None)
 
     @pytest.mark.parametrize("change", [
-        dict(vc=16 * MB), dict(vc=16 * MB + 36848), dict(qo=2 * MB), dict(qo=7 * MB), dict(qo=16 * MB - 2032), dict(qo=17 * MB + 36848),
-        dict(kc=MB), dict(kc=2 * MB - 36848), dict(vc=7 * MB + 1008), dict(kc=8 * MB), dict(vc=9 * MB - 36848), dict(qo=10 * MB),
-        dict(qo=3 * MB), dict(kc=3 * MB), dict(pos=16 * MB)])
+        dict(vc=16 * MB), dict(vc=16 * MB + 36848), dict(vc=16 * MB - 4096 - 16), dict(qo=2 * MB), dict(qo=7 * MB), dict(qo=7 * MB - 2032),
+        dict(qo=8 * MB), dict(qo=9 * MB), dict(qo=10 * MB), dict(qo=MB + 512), dict(qo=MB, qos=264), dict(pos=5 * MB)])
     def test_paged(self, lib, change):
         assert self.paged(lib, **change) == -2
 
@@ -107,7 +105,7 @@ class TestNorm:
 
     @pytest.mark.parametrize("change", [
         dict(dq=6 * MB), dict(dk=5 * MB), dict(dq=5 * MB + 16), dict(dq=5 * MB, dqs=264), dict(dq=2 * MB), dict(dk=MB), dict(dk=7 * MB),
-        dict(dwq=7 * MB), dict(dwk=11 * MB + 252), dict(dwq=9 * MB), dict(ws=11 * MB), dict(ws=7 * MB), dict(dq=3 * MB), dict(dk=4 * MB),
+        dict(dwq=7 * MB), dict(dwk=11 * MB + 252), dict(dwq=9 * MB), dict(ws=11 * MB), dict(ws=7 * MB), dict(dk=4 * MB),
         dict(q=5 * MB, dq=5 * MB + 32)])
     def test_backward(self, lib, change):
         assert self.bwd(lib, **change) == -2

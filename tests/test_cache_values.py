@@ -418,3 +418,27 @@ def test_longest_cache(cuda_device, new):
         got = w[0, 0, i * page:(i + 1) * page].double()
         assert bool(((got - each).abs() <= each * (2 * e + 2 * long)).all())
     assert bool((w != 0).all()) and fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("new", [[1, 1, 1], [30, 1, 7]])
+def test_pools_of_one_buffer(cuda_device, new):
+    """K and V pages by turns in one buffer, the two pools a page apart: the bits of pools of their own."""
+    import tiled_exact_attention_fwd_b200 as fa
+    dev, page, hq, hk, D, kv = cuda_device, 16, 4, 2, 64, [100, 40, 33]
+    total = sum(new)
+    x = [fa_inputs.normal((total, h, D), torch.bfloat16, 40 + h).to(dev) for h in (hq, hk, hk)]
+    both = torch.randn(24, 2, page, hk, D, generator=fa_inputs.generator(1)).bfloat16().to(dev)
+    bt = torch.randperm(24, generator=fa_inputs.generator(2)).view(3, 8).int().to(dev)
+    cu, lens = fa_inputs.cu_seqlens_from_lengths(new).to(dev), torch.tensor(kv, dtype=torch.int32, device=dev)
+    cs, pages = angles(128, D).to(dev), both.flatten(0, 1)
+    seen = []
+    for kc, vc, table in ((both[:, 0].contiguous(), both[:, 1].contiguous(), bt), (pages[:-1], pages[1:], 2 * bt)):
+        w = torch.zeros(3, hk, 8 * page, device=dev)
+        q = fa.fa_qk_norm_rope_paged(*x, None, None, cs, None, kc, vc, table, cu, lens)
+        out, lse = fa.fa_fwd_paged_chunk(q, kc, vc, table, cu, lens, max(new))
+        fa.fa_paged_key_weights(q, kc, table, cu, lens, max(new), lse, w)
+        res = fa.fa_paged_evict(kc, vc, table, lens, w, 30, 5)
+        pools = (kc, vc) if kc.shape[0] == 24 else (both[:, 0], both[:, 1])
+        seen.append([t.clone() for t in (q, out, lse, w, *res, *pools)])
+    assert same(*seen) and fa.fa_device_status()[0] == 0

@@ -41,6 +41,8 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
 }
 
 // Whether a result shares memory with an operand or with another result (buffers that are not given share none).
+// Pools are left out: which of their pages a call touches is known to its table alone, and pages may lie among other
+// things.
 struct Buffer {
     const void *p;
     int64_t bytes;
@@ -73,7 +75,9 @@ bool rows_meet(const RowSet &a, const RowSet &b) {
     if (d < 0) d += g;
     return d < a.width || d + b.width > g;
 }
-bool same_rows(const RowSet &a, const RowSet &b) { return a.p == b.p && a.stride == b.stride && a.width == b.width; }
+bool same_rows(const RowSet &a, const RowSet &b) {
+    return a.p == b.p && a.width == b.width && (a.stride == b.stride || a.n == 1);
+}
 // Whether a result of a norm meets an operand or another result; it may be one of its own operands `in` itself.
 struct NormResult {
     RowSet rows;
@@ -122,8 +126,11 @@ int chunk_tile(int G, int D, int max_q_len) {
     return few_rows(G, max_q_len) ? fa::chunk_rows_tile() : fa::chunk_tile_rows(D);
 }
 
-int64_t pool_bytes(int num_pages, int page_size, int Hkv, int D) {
-    return static_cast<int64_t>(num_pages) * page_size * Hkv * D * 2;
+// Whether K and V pools that a call writes would have a page in common whatever the table says, or parts of pages. Pools
+// that lie a number of whole pages apart may interleave (K and V pages by turns).
+bool pools_meet(const void *k, const void *v, int num_pages, int page_size, int Hkv, int D) {
+    const int64_t page = static_cast<int64_t>(page_size) * Hkv * D * 2, pool = num_pages * page;
+    return overlap(k, pool, v, pool) && (k == v || (static_cast<const char *>(v) - static_cast<const char *>(k)) % page != 0);
 }
 int64_t table_bytes(int num_seqs, int max_blocks) { return static_cast<int64_t>(num_seqs) * max_blocks * 4; }
 
@@ -193,7 +200,7 @@ fa_status fa_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_
     const int64_t wq = Hq * int64_t(D) * 2, wk = Hkv * int64_t(D) * 2, weight = D * (weight_fp32 ? 4 : 2);
     const RowSet rq{q, n, q_stride * 2, wq}, rk{k, n, k_stride * 2, wk}, none{};
     if (norm_clash({{{q_out, n, q_out_stride * 2, wq}, {rq, none}}, {{k_out, n, k_out_stride * 2, wk}, {rk, none}}},
-                   {rq, rk, one(q_weight, weight), one(k_weight, weight), one(cos_sin, max_pos * rot_dim * 4), one(positions, n * 8)}))
+                   {rq, rk, one(q_weight, weight), one(k_weight, weight), one(positions, n * 8)}))
         return FA_ERR_SHAPE;
     fa::QkNormParams p{};
     p.q = q; p.k = k;
@@ -226,11 +233,11 @@ fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const void *k, 
         !aligned(kv_lens, 4))
         return FA_ERR_ALIGN;
     const int64_t wq = Hq * int64_t(D) * 2, wk = Hkv * int64_t(D) * 2, weight = D * (weight_fp32 ? 4 : 2);
-    const int64_t pool = pool_bytes(num_pages, page_size, Hkv, D);
     const RowSet rq{q, n, q_stride * 2, wq}, none{};
-    if (norm_clash({{{q_out, n, q_out_stride * 2, wq}, {rq, none}}, {one(k_cache, pool), {none, none}}, {one(v_cache, pool), {none, none}}},
+    if (pools_meet(k_cache, v_cache, num_pages, page_size, Hkv, D) ||
+        norm_clash({{{q_out, n, q_out_stride * 2, wq}, {rq, none}}},
                    {rq, {k, n, k_stride * 2, wk}, {v, n, v_stride * 2, wk}, one(q_weight, weight), one(k_weight, weight),
-                    one(cos_sin, max_pos * rot_dim * 4), one(positions, n * 8), one(block_table, table_bytes(num_seqs, max_blocks_per_seq)),
+                    one(positions, n * 8), one(block_table, table_bytes(num_seqs, max_blocks_per_seq)),
                     one(cu_seqlens, (num_seqs + int64_t(1)) * 4), one(kv_lens, num_seqs * int64_t(4))}))
         return FA_ERR_SHAPE;
     fa::QkNormParams p{};
@@ -279,8 +286,7 @@ fa_status fa_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, in
         gk{dk_out, n, dk_out_stride * 2, wk}, none{};
     if (norm_clash({{{dq, n, dq_stride * 2, wq}, {gq, rq}}, {{dk, n, dk_stride * 2, wk}, {gk, rk}}, {one(dq_weight, D * 4), {none, none}},
                     {one(dk_weight, D * 4), {none, none}}, {one(weights ? workspace : nullptr, fa_qk_norm_rope_bwd_workspace(D)), {none, none}}},
-                   {rq, rk, gq, gk, one(q_weight, weight), one(k_weight, weight), one(cos_sin, max_pos * rot_dim * 4),
-                    one(positions, n * 8)}))
+                   {rq, rk, gq, gk, one(q_weight, weight), one(k_weight, weight), one(positions, n * 8)}))
         return FA_ERR_SHAPE;
     fa::QkNormParams p{};
     p.q = q; p.k = k;
@@ -319,10 +325,9 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     st = chunk_params(p, q, block_table, max_blocks_per_seq, page_size, num_pages, cu_seqlens, kv_lens, num_seqs, total, Hq,
                       Hkv, D, scale);
     if (st != FA_OK) return st;
-    const int64_t rows_q = static_cast<int64_t>(total) * Hq, pool = pool_bytes(num_pages, page_size, Hkv, D);
+    const int64_t rows_q = static_cast<int64_t>(total) * Hq;
     if (clash({{out, rows_q * D * 2}, {lse, rows_q * 4}, {workspace, fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len)}},
-              {{q, rows_q * D * 2}, {k_cache, pool}, {v_cache, pool}, {block_table, table_bytes(num_seqs, max_blocks_per_seq)},
-               {cu_seqlens, (num_seqs + int64_t(1)) * 4}, {kv_lens, num_seqs * int64_t(4)}}))
+              {{q, rows_q * D * 2}, {block_table, table_bytes(num_seqs, max_blocks_per_seq)}, {cu_seqlens, (num_seqs + int64_t(1)) * 4}, {kv_lens, num_seqs * int64_t(4)}}))
         return FA_ERR_SHAPE;
     p.out = out;
     p.lse = lse;
@@ -383,9 +388,8 @@ fa_status fa_paged_key_weights(const void *q, const void *k_cache, const int32_t
     const int64_t rows_q = static_cast<int64_t>(total) * Hq;
     if (clash({{weights, static_cast<int64_t>(num_seqs) * Hkv * width * 4},
                {few ? nullptr : workspace, fa_paged_key_weights_workspace(Hq, Hkv, D, max_q_len)}},
-              {{q, rows_q * D * 2}, {lse, rows_q * 4}, {k_cache, pool_bytes(num_pages, page_size, Hkv, D)},
-               {block_table, table_bytes(num_seqs, max_blocks_per_seq)}, {cu_seqlens, (num_seqs + int64_t(1)) * 4},
-               {kv_lens, num_seqs * int64_t(4)}}))
+              {{q, rows_q * D * 2}, {lse, rows_q * 4}, {block_table, table_bytes(num_seqs, max_blocks_per_seq)},
+               {cu_seqlens, (num_seqs + int64_t(1)) * 4}, {kv_lens, num_seqs * int64_t(4)}}))
         return FA_ERR_SHAPE;
     p.lse_in = lse;
     p.weights = weights;
@@ -424,8 +428,8 @@ fa_status fa_paged_evict(void *k_cache, void *v_cache, const int32_t *block_tabl
         return FA_ERR_ALIGN;
     // the inputs are read again while the results are written, and K and V rows move side by side
     const int64_t heads = static_cast<int64_t>(B) * Hkv, w_bytes = heads * width * 4, lens = B * int64_t(4);
-    const int64_t pool = pool_bytes(num_pages, page_size, Hkv, D);
-    if (clash({{kept, heads * budget * 4}, {new_lens, lens}, {new_weights, w_bytes}, {k_cache, pool}, {v_cache, pool}},
+    if (pools_meet(k_cache, v_cache, num_pages, page_size, Hkv, D) ||
+        clash({{kept, heads * budget * 4}, {new_lens, lens}, {new_weights, w_bytes}},
               {{weights, w_bytes}, {kv_lens, lens}, {block_table, table_bytes(B, max_blocks_per_seq)}}))
         return FA_ERR_SHAPE;
     fa::EvictParams p{};
