@@ -316,7 +316,7 @@ FA_API fa_status fa_qk_norm_rope_paged(const void *q, int64_t q_stride, const vo
  *   k_cache, v_cache, block_table, max_blocks_per_seq, page_size, num_pages: as fa_fwd_paged, pages
  *                of (page_size, Hkv, D). Entries past ceil(kv_lens[b] / page_size) are never read;
  *                what a page holds past the sequence's last key does not matter (NaN included). A value
- *                of V within it that is not finite reaches rows that do not see its key too (0 times it).
+ *                of V within it that is not finite may reach rows that do not see its key too (0 times it).
  *   kv_lens      device int32 [num_seqs]: keys of each sequence, the new tokens' own included, at most
  *                2^31 - 2^16. Sequences may share pages.
  *   causal       nonzero: new token i of n sees keys 0 .. kv_lens[b] - n + i (aligned at the end);

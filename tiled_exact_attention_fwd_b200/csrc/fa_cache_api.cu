@@ -85,9 +85,13 @@ struct NormResult {
 };
 bool norm_clash(std::initializer_list<NormResult> results, std::initializer_list<RowSet> operands) {
     for (const NormResult *r = results.begin(); r != results.end(); ++r) {
+        auto itself = [&](const RowSet &o) {
+            for (const RowSet &in : r->in)
+                if (in.p && same_rows(in, o) && same_rows(r->rows, o)) return true;
+            return false;
+        };
         for (const RowSet &o : operands)
-            if (rows_meet(r->rows, o) && !(same_rows(r->rows, o) && ((r->in[0].p && same_rows(r->in[0], o)) || (r->in[1].p && same_rows(r->in[1], o)))))
-                return true;
+            if (rows_meet(r->rows, o) && !itself(o)) return true;
         for (const NormResult *o = results.begin(); o != r; ++o)
             if (rows_meet(r->rows, o->rows)) return true;
     }
@@ -327,7 +331,8 @@ fa_status fa_fwd_paged_chunk(const void *q, const void *k_cache, const void *v_c
     if (st != FA_OK) return st;
     const int64_t rows_q = static_cast<int64_t>(total) * Hq;
     if (clash({{out, rows_q * D * 2}, {lse, rows_q * 4}, {workspace, fa_fwd_paged_chunk_workspace(Hq, Hkv, D, max_q_len)}},
-              {{q, rows_q * D * 2}, {block_table, table_bytes(num_seqs, max_blocks_per_seq)}, {cu_seqlens, (num_seqs + int64_t(1)) * 4}, {kv_lens, num_seqs * int64_t(4)}}))
+              {{q, rows_q * D * 2}, {block_table, table_bytes(num_seqs, max_blocks_per_seq)},
+               {cu_seqlens, (num_seqs + int64_t(1)) * 4}, {kv_lens, num_seqs * int64_t(4)}}))
         return FA_ERR_SHAPE;
     p.out = out;
     p.lse = lse;
